@@ -40,7 +40,8 @@
  *   work queued ahead of the call has completed.
  * - Element types: LOSA_BF16 (bfloat16) or LOSA_F32 (float) for Q, K, V and
  *   the page metadata; the cached prefix state, the outputs and all
- *   accumulation are fp32.
+ *   accumulation are fp32.  The prefix K and V may also be held in 8 bits
+ *   (the calls whose names hold quant, below).
  * - Sizes:  S sequences, Hq query heads, Hkv KV heads (G = Hq / Hkv query
  *   heads share KV head g = h / G), d = head_dim, L = prefix_len,
  *   ps = page_size, P = ceil(L / ps) pages (the last may be partial),
@@ -85,7 +86,8 @@ extern "C" {
 
 /* ---- workspace kinds -------------------------------------------------- */
 #define LOSA_WS_DENSE 0
-#define LOSA_WS_STEP  1
+#define LOSA_WS_STEP  1   /* losa_step, losa_step_ref and their _quant forms */
+#define LOSA_WS_DENSE_QUANT 2
 
 /* Problem shape shared by every call.  Limits checked by the library:
  * head_dim == 128, page_size == 16 (LOSA_ERR_UNSUPPORTED otherwise);
@@ -125,8 +127,9 @@ typedef struct {
  * records, then the page-norm rows. */
 size_t losa_page_meta_size(const losa_shape* shape);
 
-/* Bytes of workspace needed by losa_dense_prefix (which = LOSA_WS_DENSE) or
- * losa_step (LOSA_WS_STEP).  0 for an invalid shape. */
+/* Bytes of workspace needed by losa_dense_prefix (which = LOSA_WS_DENSE),
+ * losa_dense_prefix_quant (LOSA_WS_DENSE_QUANT) or the step calls
+ * (LOSA_WS_STEP).  0 for an invalid shape. */
 size_t losa_workspace_size(const losa_shape* shape, int which);
 
 /*
@@ -259,6 +262,113 @@ int losa_step_ref(const losa_shape* shape, const void* q_cur, void* q_ref,
                   const void* k_blk, const void* v_blk, float* o_p, float* l_p, float* out,
                   float* out_lse, int32_t* active_idx, int32_t* page_idx, int32_t* union_count,
                   void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- the prefix cache in 8 bits ----------------------------------------
+ * The prefix K and V may be held as 8-bit codes instead of `dtype` elements:
+ * half the bytes of a bf16 prefix to keep and to read in every pass.
+ *
+ *   k8, v8            [S][Hkv][Lc][d] e4m3 codes (OCP FP8 E4M3: no infinities,
+ *                     largest number 448, code 0x7f / 0xff = NaN)
+ *   k_scale, v_scale  [S][Hkv][Pc] fp32: one scale for each page (ps tokens)
+ *                     of each KV head
+ *
+ * A cached element stands for code * scale.  losa_quantize_prefix and
+ * losa_append_block_quant write the scale
+ *
+ *   the smallest power of two >= 2^-100 with (largest magnitude of the page's
+ *   tokens) <= 448 * scale;  1 for a page of zeros,
+ *
+ * and codes rounded to nearest, ties to even.  A power of two adds no rounding
+ * of its own: reading a code back in bf16 or fp32 is exact, and re-encoding a
+ * page with a larger scale changes only elements that fall below e4m3's normal
+ * range.  Magnitudes above 448 * 2^119 (infinities among them) are stored as
+ * that; a NaN stays NaN and does not count for the scale.
+ *
+ * Everything else keeps its type: queries, the block's K and V and the page
+ * metadata are `dtype`, the prefix state and the outputs fp32.  The page
+ * metadata that these calls write are the records of the keys that the cache
+ * holds, code * scale, so that the bound stays a bound of what is attended to.
+ *
+ * The calls that read a cache take any finite scales, also ones written by
+ * another program, of which the V scales are >= 0 (a V scale below 2^-100 is
+ * taken as 2^-100).  Scales and codes of pages and tokens past a sequence's
+ * length are never used, whatever they hold, and never written.
+ * Scale arrays need the alignment of a float only (a layer's slice of a larger
+ * array), the other buffers 16 bytes as everywhere. */
+
+/*
+ * Quantise a whole prefix: codes and scales of every token < L_s, and the page
+ * metadata of the result (what losa_build_page_meta gives for the prefix that
+ * losa_dequantize_prefix reads back; the norms are upper bounds that may differ
+ * in their last bits).
+ *
+ *   k_prefix,
+ *   v_prefix   [S][Hkv][Lc][d]  element type `dtype` (tokens < L read)
+ *   k8, v8, k_scale, v_scale  out, as above
+ *   page_meta  out, or NULL: not wanted
+ */
+int losa_quantize_prefix(const losa_shape* shape, const void* k_prefix, const void* v_prefix,
+                         void* k8, void* v8, float* k_scale, float* v_scale, void* page_meta,
+                         void* stream);
+
+/*
+ * losa_append_block for a quantised prefix: the block's keys and values become
+ * tokens L_s .. L_s+B-1 of every (s, g).  The pages those positions touch are
+ * encoded as losa_quantize_prefix encodes them, from the block's tokens and,
+ * where the first of them holds older tokens too, from what those read back as:
+ * older tokens keep their values exactly, unless a larger token of the block
+ * raises the page's scale (they are then rounded to the new one).  Their
+ * metadata records are rebuilt; page_meta may be NULL: not kept.  Arguments,
+ * sizes and errors otherwise as losa_append_block.
+ */
+int losa_append_block_quant(const losa_shape* shape, const void* k_blk, const void* v_blk,
+                            void* k8, void* v8, float* k_scale, float* v_scale, void* page_meta,
+                            void* stream);
+
+/*
+ * Read a quantised prefix back: code * scale of every token < L_s, rounded to
+ * `dtype` (exact for the scales that this library writes).
+ *
+ *   k_prefix,
+ *   v_prefix   out [S][Hkv][Lc][d]  tokens past a sequence's length are not
+ *              written
+ */
+int losa_dequantize_prefix(const losa_shape* shape, const void* k8, const void* v8,
+                           const float* k_scale, const float* v_scale, void* k_prefix,
+                           void* v_prefix, void* stream);
+
+/*
+ * losa_dense_prefix over a quantised prefix: dense attention of the block's B
+ * queries over the cached prefix and the block itself.  With block_size = 1 it
+ * is the attention of one decoded token.  Same arguments and results, with the
+ * prefix as codes and scales.
+ *
+ *   workspace  >= losa_workspace_size(shape, LOSA_WS_DENSE_QUANT) bytes,
+ *              256-byte aligned; contents on entry are irrelevant.
+ */
+int losa_dense_prefix_quant(const losa_shape* shape, const void* q, const void* k8,
+                            const void* v8, const float* k_scale, const float* v_scale,
+                            const void* k_blk, const void* v_blk, float* o_p, float* l_p,
+                            float* out, float* out_lse, void* workspace, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * losa_step and losa_step_ref over a quantised prefix: the same selection (from
+ * page_meta) and the same results, with the selected pages read as codes and
+ * scales.  Workspace: LOSA_WS_STEP.
+ */
+int losa_step_quant(const losa_shape* shape, const void* q_cur, const void* q_prev,
+                    const void* k8, const void* v8, const float* k_scale, const float* v_scale,
+                    const void* page_meta, const void* k_blk, const void* v_blk, float* o_p,
+                    float* l_p, float* out, float* out_lse, int32_t* active_idx,
+                    int32_t* page_idx, int32_t* union_count, void* workspace, size_t ws_bytes,
+                    void* stream);
+int losa_step_ref_quant(const losa_shape* shape, const void* q_cur, void* q_ref, const void* k8,
+                        const void* v8, const float* k_scale, const float* v_scale,
+                        const void* page_meta, const void* k_blk, const void* v_blk, float* o_p,
+                        float* l_p, float* out, float* out_lse, int32_t* active_idx,
+                        int32_t* page_idx, int32_t* union_count, void* workspace,
+                        size_t ws_bytes, void* stream);
 
 /* Size of the scratch array behind losa_step_noalloc: 8 MiB per GPU. */
 #define LOSA_NOALLOC_SCRATCH_BYTES (8u * 1024u * 1024u)

@@ -28,11 +28,14 @@ LOSA_BF16 = 1
 LOSA_STEP_ATTEND_UNION = 1  # losa_shape.flags: active rows attend to the group's whole union
 LOSA_WS_DENSE = 0
 LOSA_WS_STEP = 1
+LOSA_WS_DENSE_QUANT = 2
 
 #: every symbol ``include/losa.h`` declares
 EXPORTS = ("losa_page_meta_size", "losa_workspace_size", "losa_build_page_meta",
            "losa_dense_prefix", "losa_step", "losa_step_ref", "losa_step_noalloc",
-           "losa_append_block",
+           "losa_append_block", "losa_quantize_prefix", "losa_append_block_quant",
+           "losa_dequantize_prefix", "losa_dense_prefix_quant", "losa_step_quant",
+           "losa_step_ref_quant",
            "losa_read_device_status", "losa_noalloc_read_status",
            "losa_status_string", "losa_last_error")
 
@@ -76,6 +79,11 @@ class Shape(ctypes.Structure):
     def capacity(self):
         """Tokens per (sequence, KV head) in the prefix buffers."""
         return self.prefix_capacity if self.prefix_capacity > 0 else self.prefix_len
+
+    @property
+    def capacity_pages(self):
+        """Pages per (sequence, KV head) in the metadata and the scales of an 8-bit prefix."""
+        return (self.capacity + self.page_size - 1) // self.page_size
 
     @property
     def pages_per_row(self):
@@ -141,6 +149,18 @@ def lib():
         L.losa_append_block.restype = i32
         L.losa_step_ref.argtypes = [sp] + [vp] * 14 + [vp, sz, vp]
         L.losa_step_ref.restype = i32
+        L.losa_quantize_prefix.argtypes = [sp] + [vp] * 8
+        L.losa_quantize_prefix.restype = i32
+        L.losa_append_block_quant.argtypes = [sp] + [vp] * 8
+        L.losa_append_block_quant.restype = i32
+        L.losa_dequantize_prefix.argtypes = [sp] + [vp] * 7
+        L.losa_dequantize_prefix.restype = i32
+        L.losa_dense_prefix_quant.argtypes = [sp] + [vp] * 11 + [vp, sz, vp]
+        L.losa_dense_prefix_quant.restype = i32
+        L.losa_step_quant.argtypes = [sp] + [vp] * 16 + [vp, sz, vp]
+        L.losa_step_quant.restype = i32
+        L.losa_step_ref_quant.argtypes = [sp] + [vp] * 16 + [vp, sz, vp]
+        L.losa_step_ref_quant.restype = i32
         L.losa_step_noalloc.argtypes = [sp] + [vp] * 14 + [vp]
         L.losa_step_noalloc.restype = i32
         L.losa_noalloc_read_status.argtypes = [vp]
@@ -331,6 +351,123 @@ def step_noalloc(sh: Shape, q_cur, q_prev, k_prefix, v_prefix, page_meta, k_blk,
             _ptr(page_idx, (sh.num_seqs, sh.n_q_heads, A, k), torch.int32, "page_idx", dev),
             _ptr(union_count, (sh.num_seqs, sh.n_kv_heads), torch.int32, "union_count", dev)]
     _check(lib().losa_step_noalloc(ctypes.byref(sh), *args, _stream(stream)))
+
+
+# ---- the prefix cache in 8 bits -------------------------------------------
+def alloc_quant_prefix(sh: Shape, device):
+    """``(k8, v8, k_scale, v_scale)``: an empty 8-bit prefix cache of the shape's
+    capacity (``torch.float8_e4m3fn`` codes, one fp32 scale per page and KV head)."""
+    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
+    sc = (sh.num_seqs, sh.n_kv_heads, sh.capacity_pages)
+    return (torch.zeros(kv, dtype=torch.float8_e4m3fn, device=device),
+            torch.zeros(kv, dtype=torch.float8_e4m3fn, device=device),
+            torch.ones(sc, dtype=torch.float32, device=device),
+            torch.ones(sc, dtype=torch.float32, device=device))
+
+
+def _quant_ptrs(sh: Shape, k8, v8, k_scale, v_scale, dev):
+    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
+    sc = (sh.num_seqs, sh.n_kv_heads, sh.capacity_pages)
+    return [_ptr(k8, kv, torch.float8_e4m3fn, "k8", dev),
+            _ptr(v8, kv, torch.float8_e4m3fn, "v8", dev),
+            _ptr(k_scale, sc, torch.float32, "k_scale", dev),
+            _ptr(v_scale, sc, torch.float32, "v_scale", dev)]
+
+
+def quantize_prefix(sh: Shape, k_prefix, v_prefix, k8, v8, k_scale, v_scale, page_meta=None,
+                    stream=None):
+    """``losa_quantize_prefix``: the prefix as e4m3 codes and page scales, and
+    (unless ``page_meta`` is None) the page metadata of the keys they stand for."""
+    dev = _call_device(sh, k_prefix)
+    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
+    args = [_ptr(k_prefix, kv, sh.torch_dtype, "k_prefix", dev),
+            _ptr(v_prefix, kv, sh.torch_dtype, "v_prefix", dev),
+            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
+            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev)]
+    _check(lib().losa_quantize_prefix(ctypes.byref(sh), *args, _stream(stream)))
+
+
+def append_block_quant(sh: Shape, k_blk, v_blk, k8, v8, k_scale, v_scale, page_meta=None,
+                       stream=None):
+    """``losa_append_block_quant``: :func:`append_block` for an 8-bit prefix."""
+    dev = _call_device(sh, k_blk)
+    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
+    args = [_ptr(k_blk, kb, sh.torch_dtype, "k_blk", dev),
+            _ptr(v_blk, kb, sh.torch_dtype, "v_blk", dev),
+            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
+            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev)]
+    _check(lib().losa_append_block_quant(ctypes.byref(sh), *args, _stream(stream)))
+
+
+def dequantize_prefix(sh: Shape, k8, v8, k_scale, v_scale, k_prefix, v_prefix, stream=None):
+    """``losa_dequantize_prefix``: read an 8-bit prefix back in the shape's dtype."""
+    dev = _call_device(sh, k8)
+    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
+    args = [*_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
+            _ptr(k_prefix, kv, sh.torch_dtype, "k_prefix", dev),
+            _ptr(v_prefix, kv, sh.torch_dtype, "v_prefix", dev)]
+    _check(lib().losa_dequantize_prefix(ctypes.byref(sh), *args, _stream(stream)))
+
+
+def dense_prefix_quant(sh: Shape, q, k8, v8, k_scale, v_scale, k_blk, v_blk, o_p, l_p, out,
+                       out_lse, workspace, stream=None):
+    """``losa_dense_prefix_quant``: :func:`dense_prefix` over an 8-bit prefix
+    (``block_size`` 1: the attention of one decoded token).  The workspace is of
+    kind ``LOSA_WS_DENSE_QUANT``."""
+    dev = _call_device(sh, q)
+    dt = sh.torch_dtype
+    qs = (sh.num_seqs, sh.n_q_heads, sh.block_size, sh.head_dim)
+    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
+    rs = qs[:3]
+    args = [_ptr(q, qs, dt, "q", dev), *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
+            _ptr(k_blk, kb, dt, "k_blk", dev), _ptr(v_blk, kb, dt, "v_blk", dev),
+            _ptr(o_p, qs, torch.float32, "o_p", dev), _ptr(l_p, rs, torch.float32, "l_p", dev),
+            _ptr(out, qs, torch.float32, "out", dev),
+            _ptr(out_lse, rs, torch.float32, "out_lse", dev),
+            _ptr(workspace, None, torch.uint8, "workspace", dev)]
+    _check(lib().losa_dense_prefix_quant(ctypes.byref(sh), *args, workspace.numel(),
+                                         _stream(stream)))
+
+
+def step_quant(sh: Shape, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk, o_p,
+               l_p, out, out_lse, workspace, active_idx=None, page_idx=None, union_count=None,
+               stream=None):
+    """``losa_step_quant``: :func:`step` over an 8-bit prefix."""
+    _step_quant_call("losa_step_quant", sh, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta,
+                     k_blk, v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx,
+                     union_count, stream)
+
+
+def step_ref_quant(sh: Shape, q_cur, q_ref, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk,
+                   o_p, l_p, out, out_lse, workspace, active_idx=None, page_idx=None,
+                   union_count=None, stream=None):
+    """``losa_step_ref_quant``: :func:`step_ref` over an 8-bit prefix."""
+    _step_quant_call("losa_step_ref_quant", sh, q_cur, q_ref, k8, v8, k_scale, v_scale, page_meta,
+                     k_blk, v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx,
+                     union_count, stream)
+
+
+def _step_quant_call(fn, sh: Shape, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta, k_blk,
+                     v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx, union_count,
+                     stream):
+    dev = _call_device(sh, q_cur)
+    dt = sh.torch_dtype
+    qs = (sh.num_seqs, sh.n_q_heads, sh.block_size, sh.head_dim)
+    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
+    rs = qs[:3]
+    A, k = sh.n_active, sh.pages_per_row
+    args = [_ptr(q_cur, qs, dt, "q_cur", dev), _ptr(q_prev, qs, dt, "q_prev", dev),
+            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
+            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev),
+            _ptr(k_blk, kb, dt, "k_blk", dev), _ptr(v_blk, kb, dt, "v_blk", dev),
+            _ptr(o_p, qs, torch.float32, "o_p", dev), _ptr(l_p, rs, torch.float32, "l_p", dev),
+            _ptr(out, qs, torch.float32, "out", dev),
+            _ptr(out_lse, rs, torch.float32, "out_lse", dev),
+            _ptr(active_idx, (sh.num_seqs, sh.n_q_heads, A), torch.int32, "active_idx", dev),
+            _ptr(page_idx, (sh.num_seqs, sh.n_q_heads, A, k), torch.int32, "page_idx", dev),
+            _ptr(union_count, (sh.num_seqs, sh.n_kv_heads), torch.int32, "union_count", dev),
+            _ptr(workspace, None, torch.uint8, "workspace", dev)]
+    _check(getattr(lib(), fn)(ctypes.byref(sh), *args, workspace.numel(), _stream(stream)))
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:

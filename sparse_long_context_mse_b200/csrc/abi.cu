@@ -129,10 +129,10 @@ int make_dims(const losa_shape* sh, int which, Dims* d) {
   size_t off = 0;
   d->off_status = off;
   off += 256;
-  if (which == LOSA_WS_DENSE) {
+  if (which == LOSA_WS_DENSE || which == LOSA_WS_DENSE_QUANT) {
     // bf16 (tensor cores, one 211-227 KB CTA per SM): one wave of whole
     // 128-key tiles; fp32: two CTAs' worth of splits per SM
-    const bool tc = sh->dtype == LOSA_BF16;
+    const bool tc = sh->dtype == LOSA_BF16 && which == LOSA_WS_DENSE;
     int nsplit = tc ? static_cast<int>(kSizingSms / SG)
                     : static_cast<int>((2 * kSizingSms + SG - 1) / SG);
     if (nsplit < 1) nsplit = 1;

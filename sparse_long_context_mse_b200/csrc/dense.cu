@@ -637,6 +637,26 @@ __global__ void __launch_bounds__(288, 1)
 }
 
 }  // namespace
+
+int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const void* v_blk,
+                        const float* part, float* o_p, float* l_p, float* out, float* out_lse,
+                        cudaStream_t st) {
+  // behind the split kernel with programmatic dependent launch: the finish
+  // CTAs stage the block's K/V while the split kernel drains
+  cudaLaunchConfig_t cf = {};
+  cudaLaunchAttribute at[1];
+  cf.gridDim = dim3(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps, 1);
+  cf.blockDim = dim3(kFinishWarps * 32, 1, 1);
+  cf.dynamicSmemBytes = 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float);
+  cf.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cf.attrs = at;
+  cf.numAttrs = 1;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cf, dense_finish_kernel, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
+  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
+}
 }  // namespace losa
 
 extern "C" int losa_dense_prefix(const losa_shape* shape, const void* q, const void* k_prefix,
@@ -696,24 +716,8 @@ extern "C" int losa_dense_prefix(const losa_shape* shape, const void* q, const v
     dense_partial_kernel<<<dim3(d.nsplit, d.S * d.Hkv), kDenseWarps * 32, 0, st>>>(
         q, k_prefix, v_prefix, part, status, d);
   }
-  {
-    // behind the split kernel with programmatic dependent launch: the finish
-    // CTAs stage the block's K/V while the split kernel drains
-    cudaLaunchConfig_t cf = {};
-    cudaLaunchAttribute at[1];
-    cf.gridDim = dim3(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps, 1);
-    cf.blockDim = dim3(kFinishWarps * 32, 1, 1);
-    cf.dynamicSmemBytes = 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float);
-    cf.stream = st;
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cf.attrs = at;
-    cf.numAttrs = 1;
-    const cudaError_t ef = cudaLaunchKernelEx(&cf, dense_finish_kernel, q, k_blk, v_blk,
-                                              static_cast<const float*>(part), o_p, l_p, out,
-                                              out_lse, d);
-    if (ef != cudaSuccess) return record_cuda_error(ef);
-  }
+  rc = launch_dense_finish(d, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, st);
+  if (rc != LOSA_OK) return rc;
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
 }

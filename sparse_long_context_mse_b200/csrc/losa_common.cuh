@@ -32,6 +32,7 @@ struct Dims {
   int Lc, Pc;             // prefix capacity: tokens (K/V row stride) and page records per (s, g)
   int all_pages;          // k == P: every page is selected, no scoring needed
   int attend_union;       // LOSA_STEP_ATTEND_UNION: active rows attend to the group's union
+  int quant;              // the prefix K and V are e4m3 codes with page scales
   const int32_t* lens;    // per-sequence prefix lengths (device, [S]) or null: every one is L
   float scale;            // softmax scale (natural-log units)
   float scale_log2;       // scale * log2(e): scores in base-2 units
@@ -232,6 +233,10 @@ inline bool bad_ptr(const void* p) {
 inline bool bad_opt_ptr(const void* p) {
   return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) != 0;
 }
+// (page scales: read and written one float at a time)
+inline bool bad_scale_ptr(const float* p) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0;
+}
 inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   if (!a || !b || !na || !nb) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -258,12 +263,19 @@ int make_dims(const losa_shape* sh, int which, Dims* d);
 bool fused_step_fits(const Dims& d, int max_dyn);
 // Dynamic shared memory a B200 CTA may opt in to (227 KB).
 constexpr int kB200MaxDynSmem = 232448;
-// The fused step kernel (step_fused.cu); arguments already validated.
+// The fused step kernel (step_fused.cu); arguments already validated.  With
+// d.quant, k_prefix and v_prefix are e4m3 codes with these page scales.
 int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, const void* k_prefix,
                       const void* v_prefix, const void* page_meta, const void* k_blk,
                       const void* v_blk, float* o_p, float* l_p, float* out, float* out_lse,
                       int32_t* active_idx, int32_t* page_idx, int32_t* union_count,
-                      void* workspace, cudaStream_t st, void* q_ref_out = nullptr);
+                      void* workspace, cudaStream_t st, void* q_ref_out = nullptr,
+                      const float* k_scale = nullptr, const float* v_scale = nullptr);
+// The dense pass's finish kernel (dense.cu): merges the split partials of
+// every row, adds the block's own keys, writes cache and output.
+int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const void* v_blk,
+                        const float* part, float* o_p, float* l_p, float* out, float* out_lse,
+                        cudaStream_t st);
 int record_cuda_error(cudaError_t e);  // stores the message, returns LOSA_ERR_CUDA
 // 2-D tensor map over a [nrows][128] bf16 tensor at `base`, for
 // 128-byte-swizzled boxes of 64 channels x box_rows rows (rows past nrows

@@ -42,6 +42,11 @@ __device__ __forceinline__ void prefetch_tmap(const void* map) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(bar)) : "memory");
 }
+// Generic-proxy shared-memory writes ordered before later accesses of
+// the async proxy (the tensor core, TMA copies).
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 // 2^x on the special-function unit (approximate, flushes denormals).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

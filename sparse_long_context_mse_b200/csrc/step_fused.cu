@@ -54,6 +54,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
 
@@ -235,9 +236,12 @@ __device__ __forceinline__ int kv_off(int key, int ch) {
 // 16 query rows at q16 ([16][256 B], chunks swizzled by row).  Row i of the
 // tile takes part iff bit i of `rows` is set; keys >= ntok are masked (their
 // V rows must be finite: the loaders zero them).
-template <bool TMA>
+// VS: the page's values are stored without their scale `vscale`; it multiplies
+// the weights of the V product instead (and a K scale comes in with sl2).
+template <bool TMA, bool VS = false>
 __device__ __forceinline__ void tile_attend(TileAcc& t, const char* q16, const char* Kp,
-                                         const char* Vp, uint32_t rows, int ntok, float sl2) {
+                                         const char* Vp, uint32_t rows, int ntok, float sl2,
+                                         float vscale = 1.f) {
   const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
   float s[2][4];
 #pragma unroll
@@ -306,7 +310,11 @@ __device__ __forceinline__ void tile_attend(TileAcc& t, const char* q16, const c
   // P (16 rows x 16 keys) as the A operand: bf16 high part and remainder
   uint32_t ah[4], al[4];
   {
-    const float pv[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+    float pv[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+    if (VS) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pv[i] *= vscale;
+    }
     float rem[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) rem[i] = pv[i] - __bfloat162float(__float2bfloat16_rn(pv[i]));
@@ -326,6 +334,50 @@ __device__ __forceinline__ void tile_attend(TileAcc& t, const char* q16, const c
     mma_bf16(t.o[2 * np + 1], ah, b2, b3);
     mma_bf16(t.o[2 * np], al, b0, b1);
     mma_bf16(t.o[2 * np + 1], al, b2, b3);
+  }
+}
+
+// 8-bit prefix: one warp turns a gathered page of K or V -- 16 x 128 e4m3 codes
+// in the last 2 KB of its slot -- into the slot's element type, in place (every
+// lane reads its codes before any lane stores).  bf16: the codes' own values in
+// the kv_off<true> layout (exact; the page scale stays a factor of the scores or
+// the weights); fp32: code * scale, plain rows.  Rows >= ntok become zero.
+template <int DT>
+__device__ __forceinline__ void expand_page(char* slot, int ntok, float scale) {
+  const int lane = threadIdx.x & 31;
+  constexpr int raw0 = kPS * kD * ((DT == LOSA_BF16 ? 2 : 4) - 1);
+  uint4 raw[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = lane + 32 * q;  // row e / 8, channels 16 (e % 8) ..
+    raw[q] = (e >> 3) < ntok ? *reinterpret_cast<const uint4*>(slot + raw0 + e * 16)
+                             : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int e = lane + 32 * q, row = e >> 3;
+    const uint32_t w[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+    if (DT == LOSA_BF16) {
+      uint32_t b[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = e4m3x4_to_f32(w[i]);
+        b[2 * i] = pack_bf16x2(f.x, f.y);
+        b[2 * i + 1] = pack_bf16x2(f.z, f.w);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<uint4*>(slot + kv_off<true>(row, 2 * (e & 7) + h)) =
+            make_uint4(b[4 * h], b[4 * h + 1], b[4 * h + 2], b[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = e4m3x4_to_f32(w[i]);
+        *reinterpret_cast<float4*>(slot + row * 512 + (e & 7) * 64 + i * 16) =
+            make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
+      }
+    }
   }
 }
 
@@ -909,6 +961,7 @@ struct StepLayout {
                        // largest half-widths [R16]
   int qn;              // active rows' 2^-14 ||q-||, 2^-14 ||q+|| [R16] float2
   int mbar;            // kMaxStages ring barriers, the queries', the gather's
+  int psc;             // 8-bit prefix: the K and V scales of the CTA's pages [max_lp] float2
   int total;
 };
 
@@ -917,8 +970,10 @@ struct StepParams {
   const void* qp;
   const char* meta;
   const float2* norms;  // the page-norm section of the metadata (row stride pn)
-  const void* K;
+  const void* K;   // 8-bit prefix: the codes
   const void* V;
+  const float* ks;  // 8-bit prefix: the page scales [S * Hkv][Pc]
+  const float* vs;
   const void* kb;
   const void* vb;
   float* o_p;
@@ -960,7 +1015,10 @@ constexpr int kMiscInts = kMiscScal + 32;
 // scalars
 constexpr int kSFail = 0, kSNlp = 1, kSWt = 4 /*[4]*/, kSWsum = 8 /*[8]*/;
 
-template <int DT>
+// Q8: the prefix K and V are e4m3 codes with a scale per page and KV head; the
+// selected pages are copied as codes (half the bytes) and expanded in shared
+// memory.
+template <int DT, bool Q8>
 __global__ void __launch_bounds__(kThreads, 1)
     losa_step_kernel(const __grid_constant__ StepParams prm,
                      const __grid_constant__ CUtensorMap kmap,
@@ -1030,6 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* gmx = reinterpret_cast<uint32_t*>(smem + lo.gmx);
   uint32_t* emx = reinterpret_cast<uint32_t*>(smem + lo.emx);
   float2* qn = reinterpret_cast<float2*>(smem + lo.qn);
+  float2* psc = reinterpret_cast<float2*>(smem + lo.psc);
   uint64_t* gbar = mbar + kMaxStages;  // [2]: the gather's two page buffers
   uint64_t* ebar = gbar + 2;            // [kMaxStages]: ring slot released by every warp
 
@@ -1038,7 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // otherwise at exit, so that its CTAs never take SMs this grid's later
   // clusters need
   if (prm.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (DT == LOSA_BF16 && tid == 0 && d.R > 0) {  // (the page gather's maps; no data read)
+  if (DT == LOSA_BF16 && !Q8 && tid == 0 && d.R > 0) {  // (the page gather's maps; no data read)
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
   }
@@ -1700,7 +1759,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto issue = [&](int bt) {
     const int b0 = bt * prm.ngp, nb = min(prm.ngp, nlp - b0);
     char* bufp = ring + (bt & 1) * prm.ngp * 2 * pbytes;
-    if (DT == LOSA_BF16) {
+    if (Q8) {
+      // the codes of the page's tokens (none past the prefix), into the last
+      // 2 KB of the page's slots (ngp <= 16: one page per lane)
+      const int p = lane < nb ? lpages[b0 + lane] : 0;
+      const uint32_t nbytes = lane < nb ? static_cast<uint32_t>(min(kPS, Ls - p * kPS) * kD) : 0u;
+      const uint32_t total = __reduce_add_sync(0xffffffffu, nbytes);
+      if (lane == 0) mbar_expect_tx(&gbar[bt & 1], 2 * total);
+      __syncwarp();
+      if (lane < nb) {
+        const size_t off = (static_cast<size_t>(sg) * d.Lc + static_cast<size_t>(p) * kPS) * kD;
+        char* dk = bufp + 2 * lane * pbytes + pbytes - kPS * kD;
+        bulk_g2s(dk, static_cast<const char*>(prm.K) + off, nbytes, &gbar[bt & 1]);
+        bulk_g2s(dk + pbytes, static_cast<const char*>(prm.V) + off, nbytes, &gbar[bt & 1]);
+      }
+    } else if (DT == LOSA_BF16) {
       if (lane == 0) mbar_expect_tx(&gbar[bt & 1], static_cast<uint32_t>(nb * 2 * pbytes));
       __syncwarp();
 #pragma unroll 1
@@ -1738,6 +1811,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nbat > 0) issue(0);
     if (nbat > 1) issue(1);
   }
+  if (Q8) {  // (read after the next block barrier)
+#pragma unroll 1
+    for (int i = tid; i < nlp; i += kThreads) {
+      const size_t o = static_cast<size_t>(sg) * d.Pc + lpages[i];
+      psc[i] = make_float2(prm.ks[o], fmaxf(prm.vs[o], kMinScale));
+    }
+  }
+  // the pages of batch bt have landed: their codes become elements
+  auto expand = [&](int bt) {
+    const int b0 = bt * prm.ngp, nb = min(prm.ngp, nlp - b0);
+    char* bufp = ring + (bt & 1) * prm.ngp * 2 * pbytes;
+#pragma unroll 1
+    for (int u = warp; u < 2 * nb; u += kWarps) {
+      const int i = b0 + (u >> 1);
+      expand_page<DT>(bufp + u * pbytes, min(kPS, Ls - lpages[i] * kPS),
+                      (u & 1) ? psc[i].y : psc[i].x);
+    }
+    fence_async_smem();  // before a later batch's copies land on these stores
+  };
   LOSA_PHASE(12);
 
   // ---- while the pages land: the block's K/V and the cached state are in
@@ -1837,7 +1929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bt == 0) LOSA_PHASE(14);
       // V rows past the sequence's end of its partial last page may hold
       // anything (P is 0 there, but 0 times NaN is NaN): zero them
-      if (Ls % kPS) {
+      if (Q8) {
+        if (__all_sync(0xffffffffu, scal[kSFail] == 0)) expand(bt);
+      } else if (Ls % kPS) {
 #pragma unroll 1
         for (int i = 0; i < nb; ++i) {
           const int p = lpages[b0 + i];
@@ -1858,8 +1952,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bits = (masks[(b0 + i) * MW + (mtg >> 1)] >> ((mtg & 1) * 16)) & 0xffffu;
           if (!bits) continue;
           const int p = lpages[b0 + i];
-          tile_attend<true>(t, qa + mtg * 16 * 256, bufp + 2 * i * pbytes,
-                            bufp + (2 * i + 1) * pbytes, bits, min(kPS, Ls - p * kPS), sl2);
+          tile_attend<true, Q8>(t, qa + mtg * 16 * 256, bufp + 2 * i * pbytes,
+                                bufp + (2 * i + 1) * pbytes, bits, min(kPS, Ls - p * kPS),
+                                Q8 ? sl2 * psc[b0 + i].x : sl2, Q8 ? psc[b0 + i].y : 1.f);
         }
       }
       __syncthreads();  // the buffer is free: the batch after next may land in it
@@ -1950,6 +2045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b0 = bt * prm.ngp, nb = min(prm.ngp, nlp - b0);
       char* bufp = ring + (bt & 1) * prm.ngp * 2 * pbytes;
       if (ok2 && scal[kSFail] == 0 && !mbar_wait(&gbar[bt & 1], (bt >> 1) & 1)) scal[kSFail] = 1;
+      if (Q8 && __all_sync(0xffffffffu, scal[kSFail] == 0)) expand(bt);
       __syncthreads();
       if (scal[kSFail] == 0) {
 #pragma unroll 1
@@ -2208,6 +2304,7 @@ bool plan_step(const Dims& d, StepParams* prm, int max_dyn, const ClusterRoom& r
       lo.emx = take(bf && sel ? 4LL * R16 : 0, 16);
       lo.qn = take(8LL * R16, 16);
       lo.mbar = take(8LL * (2 * kMaxStages + 2), 16);
+      lo.psc = take(d.quant ? 8LL * prm->max_lp : 0, 8);
       // + 1 KB: the kernel aligns its shared-memory base to 1024 bytes
       lo.total = static_cast<int>(std::min<long long>(take.off + 1024, 1LL << 30));
       if (take.off + 1024 > max_dyn) continue;
@@ -2228,9 +2325,9 @@ bool g_attr_done[kMaxDevices] = {};
 int g_attr_dyn[kMaxDevices] = {};
 ClusterRoom g_attr_room[kMaxDevices];
 
-template <int DT>
+template <int DT, bool Q8>
 cudaError_t set_attrs(int optin, int* dyn) {
-  const void* fn = reinterpret_cast<const void*>(losa_step_kernel<DT>);
+  const void* fn = reinterpret_cast<const void*>(losa_step_kernel<DT, Q8>);
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, fn);
   if (e != cudaSuccess) return e;
@@ -2258,7 +2355,7 @@ int room_for(int csize, int dyn) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, losa_step_kernel<LOSA_BF16>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, losa_step_kernel<LOSA_BF16, false>, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();  // (not sticky) a size the device cannot place
     return 0;
   }
@@ -2276,8 +2373,10 @@ int ensure_attributes(int* max_dyn, ClusterRoom* room) {
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return record_cuda_error(e);
     int dyn = optin;
-    if ((e = set_attrs<LOSA_BF16>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
-    if ((e = set_attrs<LOSA_F32>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
+    if ((e = set_attrs<LOSA_BF16, false>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
+    if ((e = set_attrs<LOSA_F32, false>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
+    if ((e = set_attrs<LOSA_BF16, true>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
+    if ((e = set_attrs<LOSA_F32, true>(optin, &dyn)) != cudaSuccess) return record_cuda_error(e);
     g_attr_dyn[dev] = dyn;
     g_attr_room[dev].c8 = room_for(kMaxCombineCtas, dyn);
     g_attr_room[dev].c16 = room_for(kMaxClusterCtas, dyn);
@@ -2300,7 +2399,8 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
                       const void* v_prefix, const void* page_meta, const void* k_blk,
                       const void* v_blk, float* o_p, float* l_p, float* out, float* out_lse,
                       int32_t* active_idx, int32_t* page_idx, int32_t* union_count,
-                      void* workspace, cudaStream_t st, void* q_ref_out) {
+                      void* workspace, cudaStream_t st, void* q_ref_out, const float* k_scale,
+                      const float* v_scale) {
   int max_dyn = 0;
   ClusterRoom room;
   int rc = ensure_attributes(&max_dyn, &room);
@@ -2318,6 +2418,8 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
   prm.pn = meta_norm_stride(d);
   prm.K = k_prefix;
   prm.V = v_prefix;
+  prm.ks = k_scale;
+  prm.vs = v_scale;
   prm.kb = k_blk;
   prm.vb = v_blk;
   prm.o_p = o_p;
@@ -2332,7 +2434,7 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
   CUtensorMap kmap, vmap;
   std::memset(&kmap, 0, sizeof(kmap));
   std::memset(&vmap, 0, sizeof(vmap));
-  if (d.dtype == LOSA_BF16 && d.R > 0) {
+  if (d.dtype == LOSA_BF16 && d.R > 0 && !d.quant) {
     // one 3-D copy per page when the driver takes the page map, else two
     // 2-D copies (one per 64-channel half)
     const unsigned long long rows = static_cast<unsigned long long>(NG) * d.Lc;
@@ -2356,9 +2458,10 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
   attr[1].val.programmaticStreamSerializationAllowed = 1;  // overlaps the previous kernel's tail
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = d.dtype == LOSA_BF16
-                            ? cudaLaunchKernelEx(&cfg, losa_step_kernel<LOSA_BF16>, prm, kmap, vmap)
-                            : cudaLaunchKernelEx(&cfg, losa_step_kernel<LOSA_F32>, prm, kmap, vmap);
+  auto* fn = d.dtype == LOSA_BF16
+                 ? (d.quant ? losa_step_kernel<LOSA_BF16, true> : losa_step_kernel<LOSA_BF16, false>)
+                 : (d.quant ? losa_step_kernel<LOSA_F32, true> : losa_step_kernel<LOSA_F32, false>);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, prm, kmap, vmap);
   return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
 }
 

@@ -74,10 +74,6 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Generic-proxy shared-memory writes made visible to the tensor core.
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // 32 consecutive fp32 columns of this thread's TMEM lane (warp w of a warp
 // group reads lanes 32w..32w+31: the lane field of taddr must be 32w).
