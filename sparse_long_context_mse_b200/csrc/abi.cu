@@ -27,7 +27,9 @@ int record_cuda_error(cudaError_t e) {
   return LOSA_ERR_CUDA;
 }
 
-int make_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsigned box_rows) {
+namespace {
+// The driver's tensor map encoder, looked up once; null if it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -38,6 +40,12 @@ int make_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsi
         q == cudaDriverEntryPointSuccess)
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
+  return encode;
+}
+}  // namespace
+
+int make_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsigned box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (!encode) return LOSA_ERR_CUDA;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), nrows};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
@@ -51,22 +59,27 @@ int make_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsi
 }
 
 int make_page_tmap(CUtensorMap* map, const void* base, unsigned long long nrows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (!encode) return LOSA_ERR_CUDA;
   const cuuint64_t dims[3] = {64u, nrows, 2u};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2, 128u};
   const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(kPS), 2u};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? LOSA_OK : LOSA_ERR_CUDA;
+}
+
+int make_byte_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsigned box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return LOSA_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), nrows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kD), box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
                             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -129,10 +142,21 @@ int make_dims(const losa_shape* sh, int which, Dims* d) {
   size_t off = 0;
   d->off_status = off;
   off += 256;
-  if (which == LOSA_WS_DENSE || which == LOSA_WS_DENSE_QUANT) {
+  if (which == LOSA_WS_DENSE_QUANT) {
+    // one CTA per SM, or two for the two halves of more than 64 fp32 rows
+    const int halves = dense_quant_halves(*d);
+    const long long tiles = (d->L + kLineKeys - 1) / kLineKeys * static_cast<long long>(SG);
+    d->line_ctas = static_cast<int>(std::min<long long>(kSizingSms / halves, tiles));
+    d->off_part = off;
+    off += align256((SG + d->line_ctas - 1) * static_cast<size_t>(G * d->B) * kPartStride *
+                    sizeof(float));
+    d->total = off;
+    return LOSA_OK;
+  }
+  if (which == LOSA_WS_DENSE) {
     // bf16 (tensor cores, one 211-227 KB CTA per SM): one wave of whole
     // 128-key tiles; fp32: two CTAs' worth of splits per SM
-    const bool tc = sh->dtype == LOSA_BF16 && which == LOSA_WS_DENSE;
+    const bool tc = sh->dtype == LOSA_BF16;
     int nsplit = tc ? static_cast<int>(kSizingSms / SG)
                     : static_cast<int>((2 * kSizingSms + SG - 1) / SG);
     if (nsplit < 1) nsplit = 1;

@@ -135,6 +135,20 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     *reinterpret_cast<float4*>(Vsb + j * kD + c) = vv;
   }
   __syncthreads();
+  // the group's partials: one per fixed split, or one per CTA whose range of
+  // the line of tiles meets the group
+  size_t first = static_cast<size_t>(sg) * d.nsplit;
+  int nparts = d.nsplit;
+  if (d.line_ctas) {
+    long long before, all;
+    line_sums(d, s, before, all);
+    const long long total = all * d.Hkv;
+    const int nt = line_tiles(d, s), n = line_ctas_used(d, total);
+    const long long x0 = before * d.Hkv + static_cast<long long>(g) * nt;
+    const int c0 = line_cta_of(x0, total, n);
+    first = static_cast<size_t>(c0) + sg;
+    nparts = line_cta_of(x0 + nt - 1, total, n) - c0 + 1;
+  }
   // launched behind the split kernel (programmatic dependent launch): its
   // partials are read only after it has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -146,18 +160,18 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     // merge the prefix partials (base-2 units) of every split in one pass,
     // kFinishBatch splits' loads in flight at a time, the running sums rescaled when
     // a batch raises the maximum
-    const float* p0 = part + (static_cast<size_t>(sg) * d.nsplit * rows + r) * kPartStride;
+    const float* p0 = part + (first * rows + r) * kPartStride;
     const size_t pstride = static_cast<size_t>(rows) * kPartStride;
     float M = -INFINITY, lsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s0 = 0; s0 < d.nsplit; s0 += kFinishBatch) {
+    for (int s0 = 0; s0 < nparts; s0 += kFinishBatch) {
       float mc[kFinishBatch], lc[kFinishBatch];
       float4 ac[kFinishBatch];
 #pragma unroll
       for (int i = 0; i < kFinishBatch; ++i) {
         mc[i] = -INFINITY;
-        if (s0 + i < d.nsplit) {
+        if (s0 + i < nparts) {
           const float* src = p0 + (s0 + i) * pstride;
           mc[i] = __ldcg(src);
           lc[i] = __ldcg(src + 1);
@@ -175,7 +189,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
       acc.w *= rs;
 #pragma unroll
       for (int i = 0; i < kFinishBatch; ++i) {
-        if (s0 + i < d.nsplit) {
+        if (s0 + i < nparts) {
           const float w = exp2f(mc[i] - Mh);
           lsum += w * lc[i];
           acc.x += w * ac[i].x;

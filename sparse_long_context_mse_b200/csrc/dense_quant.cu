@@ -2,86 +2,733 @@
 //
 // s_j = scale * ks(page j) * (q . k8_j);  o = sum_j e^(s_j - m) vs(page j) v8_j
 // / sum_j e^(s_j - m): the page scales are factors of a key's score and of its
-// value.  Flash-decode layout as in dense.cu: one CTA streams a range of pages
-// for all G*B query rows of a KV head and writes an online-softmax partial per
-// row; the finish kernel merges them.
+// value.  In base 2, with x_j = s_j log2(e) + log2 vs_j and a reference m' per
+// row, the kernel accumulates
+//
+//   w_j = 2^(x_j - m'),   O = sum_j w_j v8_j,   l = sum_j w_j / vs_j,   o = O / l,
+//
+// so that one reference bounds what is accumulated, however different the V
+// scales of the pages are: a page of small values that holds the weight keeps
+// its relative accuracy.
+//
+// What bounds it is HBM: 256 bytes per key and KV head, read once.  The work is
+// laid out so that nothing on the chip takes longer:
+//
+// * Keys are the rows of both products (M = 128, one tile), the G*B query rows
+//   are the columns (N = 16 .. 128): few query rows cost little, one decoded
+//   token as well as a block of 32.
+// * S^T = K8 Q^T runs on the codes as TMA brought them (kind::f8f6f4, e4m3 times
+//   e4m3): nothing converts K.  Q enters as a sum of e4m3 parts, each the
+//   rounding of what the parts before it left: a bf16 number has 8 significant
+//   bits, two parts of 4 hold it exactly; fp32 takes six, the last three 2^12
+//   times larger in an accumulator of their own.  Rows are scaled by a power of
+//   two to a maximum in [128, 256), so that two parts reach down to 2^-18 of the
+//   row's maximum (six: 2^-30).
+// * O^T = V8^T W: W in fp16 (its rounding, and the rounding's remainder as a
+//   second fp16 operand: 22 bits), so V8 has to be fp16 too.  Four warps
+//   transpose V codes out of shared memory (ldmatrix, bytes), widen them (exact)
+//   and store them as the A operand in TMEM, which costs 1/8 of the shared-memory
+//   traffic of an fp16 tile there; W goes through shared memory as the MN-major B.
+// * A softmax thread owns one key (TMEM lane) and half of the query columns: the
+//   page scales are constants of the thread, l is a sum in registers across tiles
+//   (joined over the lanes at the end), and no tile needs a maximum over the
+//   lanes: the reference moves only when some w would pass 2^15, which one
+//   barrier with a vote finds out.
+// * The tensor core's accumulator truncates (up to 2^-24 of it on each of the 16
+//   steps of a tile, all in one direction: 1.4e-5 after 800 of them, measured),
+//   so O stays in it for one tile only and is summed in registers.
+// * All SMs get the same number of tiles, whatever the lengths and the number of
+//   KV heads (the line of tiles, losa_common.cuh).
 #include "e4m3.cuh"
 #include "losa_common.cuh"
+#include "ptx.cuh"
+#include "umma.cuh"
 
 namespace losa {
 namespace {
 
-constexpr int kWarpsQ = 8;
-constexpr int kRowsQ = 8;  // query rows per warp
+// Warps 0-7: softmax; 8-11: V to fp16; 12 loads, 13 issues MMAs, 14 prepares the
+// tiles' scales, 15 has nothing to do.  The first two warp groups take registers
+// over from the other two: 256 x 192 + 256 x 64 = the launch's 512 x 128.
+constexpr int kSoftmaxThreads = 256;
+constexpr int kThreadsQ = 512;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+static_assert(256 * (kSoftmaxRegs + kOtherRegs) == kThreadsQ * 128, "register split");
+constexpr int kTileBytes = kLineKeys * kD;  // one K or V tile of codes: 16 KB
+constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (fp16 pairs)
+constexpr float kRefTop = 11.f;             // a new reference puts the row's maximum at 2^11 ..
+constexpr float kRefMove = 15.f;            // .. and stays until a weight would pass 2^15
+constexpr float kPartScale = 4096.f;        // fp32: parts 4-6 are this much larger
 
-// One page of codes into shared memory as fp32 values, rows >= ntok zero.
-__device__ __forceinline__ void load_page_e4m3(const uint8_t* src, float s, int ntok, float* dst) {
-  const int j = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;  // 256 threads: 16 rows x 16 chunks
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-  if (j < ntok) {
-    const uint2 w = *reinterpret_cast<const uint2*>(src + j * kD + c);
-    a = e4m3x4_to_f32(w.x);
-    b = e4m3x4_to_f32(w.y);
-  }
-  float4* o = reinterpret_cast<float4*>(dst + j * kD + c);
-  o[0] = make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
-  o[1] = make_float4(b.x * s, b.y * s, b.z * s, b.w * s);
+typedef unsigned long long u64;
+
+// Pairs of fp32 numbers in one 64-bit register pair.
+__device__ __forceinline__ u64 pk(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 up(u64 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-__global__ void __launch_bounds__(kWarpsQ * 32)
-    dense_quant_partial_kernel(const void* __restrict__ Q, const uint8_t* __restrict__ K,
-                               const uint8_t* __restrict__ V, const float* __restrict__ ks,
-                               const float* __restrict__ vs, float* __restrict__ part,
-                               int* __restrict__ status, Dims d) {
-  __shared__ __align__(16) float Ks[kPS * kD];
-  __shared__ __align__(16) float Vs[kPS * kD];
-  __shared__ float Ps[kWarpsQ][kPS];
-  const int sg = blockIdx.y, split = blockIdx.x;
-  const int s = sg / d.Hkv, g = sg % d.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = d.G * d.B;
-  const int L = seq_len(d, s);
-  const int p0 = split * d.split_pages;
-  const int p1 = min((L + kPS - 1) / kPS, p0 + d.split_pages);
-  if (split == 0 && threadIdx.x == 0 && seq_len_bad(d, s)) atomicCAS(status, 0, LOSA_ERR_DEVICE_BOUNDS);
-  for (int rbase = 0; rbase < rows; rbase += kWarpsQ * kRowsQ) {
-    float4 q[kRowsQ], acc[kRowsQ];
-    float m[kRowsQ], l[kRowsQ];
-#pragma unroll
-    for (int i = 0; i < kRowsQ; ++i) {
-      const int r = rbase + warp * kRowsQ + i;
-      const int rr = r < rows ? r : 0;
-      const int h = g * d.G + rr / d.B, t = rr % d.B;
-      q[i] = ld4(Q, ((static_cast<size_t>(s) * d.Hq + h) * d.B + t) * kD + 4 * lane, d.dtype);
-      acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
-    for (int p = p0; p < p1; ++p) {
-      const int ntok = min(kPS, L - p * kPS);
-      const size_t off = (static_cast<size_t>(sg) * d.Lc + static_cast<size_t>(p) * kPS) * kD;
-      const size_t sp = static_cast<size_t>(sg) * d.Pc + p;
-      __syncthreads();
-      load_page_e4m3(K + off, ks[sp], ntok, Ks);
-      load_page_e4m3(V + off, fmaxf(vs[sp], kMinScale), ntok, Vs);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kRowsQ; ++i)
-        if (rbase + warp * kRowsQ + i < rows)
-          attend_page_row(q[i], Ks, Vs, ntok, d.scale_log2, m[i], l[i], acc[i], Ps[warp]);
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsQ; ++i) {
-      const int r = rbase + warp * kRowsQ + i;
-      if (r >= rows) continue;
-      float* dst = part + ((static_cast<size_t>(sg) * d.nsplit + split) * rows + r) * kPartStride;
-      if (lane == 0) {
-        dst[0] = m[i];
-        dst[1] = l[i];
-      }
-      *reinterpret_cast<float4*>(dst + 4 + 4 * lane) = acc[i];
-    }
+// NR: query columns (MMA N); NQ: e4m3 parts of a query row (2: bf16, 6: fp32).
+template <int NR, int NQ>
+struct QPlan {
+  static constexpr int ch = NR / 2;                      // columns per softmax warp group
+  static constexpr int cw = ch < 32 ? ch : 32;           // columns handled at a time
+  static constexpr int nch = ch / cw;
+  static constexpr int na = NQ > 3 ? 2 : 1;              // score accumulators
+  static constexpr int ob = NR > 64 ? 1 : 2;             // O buffers
+  static constexpr int atom = kLineKeys * 128;           // 64 fp16 columns of W: 16 KB
+  static constexpr int watoms = NR > 64 ? 2 : 1;
+  static constexpr int wbytes = 2 * watoms * atom;       // W and its remainder
+  static constexpr int qbytes = NQ * NR * kD;
+  static constexpr int small = 3072;                     // barriers, row factors, exchange
+  static constexpr int room = kB200MaxDynSmem - small - qbytes - 2 * wbytes;
+  static constexpr int st = room / (2 * kTileBytes) < 4 ? room / (2 * kTileBytes) : 4;
+  static constexpr int nbars = 7 + 4 * st;
+  static constexpr int smem = qbytes + 2 * wbytes + 2 * st * kTileBytes + small;
+  static constexpr uint32_t tS = 0, tO = 2 * na * NR, tV = tO + ob * NR, cols = 512;
+  static_assert(st >= 2 && smem <= kB200MaxDynSmem, "shared memory");
+  static_assert(tV + 2 * kVCols <= 512, "TMEM");
+  static_assert(nbars * 8 + 8 + 2 * NR * 4 + 2 * 4 * 32 * 4 + 2 * 32 * 4 + 2 * 144 + 64 <= small,
+                "small area");
+};
+
+// What the softmax warps have to know of a tile.
+struct __align__(16) TileInfo {
+  float4 page[kLineKeys / kPS];  // score factor, log2 and reciprocal of the value scale
+  int nv;                        // real keys
+  int last;                      // the KV head's last tile in this CTA
+  int pad[2];
+};
+
+// A CTA's place on the line of tiles.
+struct LinePos {
+  int s, g, lt, nt, L;  // sequence, KV head, tile of it, its number of tiles, its keys
+  __device__ __forceinline__ void start(const Dims& d) {
+    L = seq_len(d, s);
+    nt = (L + kLineKeys - 1) / kLineKeys;
   }
+  __device__ __forceinline__ void next_head(const Dims& d) {
+    lt = 0;
+    if (++g < d.Hkv) return;
+    g = 0;
+    if (++s < d.S) start(d);
+  }
+  __device__ __forceinline__ void next(const Dims& d) {
+    if (++lt == nt) next_head(d);
+  }
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
+template <int NR, int NQ>
+__global__ void __launch_bounds__(kThreadsQ, 1)
+    dense_quant_kernel(const void* __restrict__ Q, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap, const float* __restrict__ ks,
+                       const float* __restrict__ vs, float* __restrict__ part,
+                       int* __restrict__ status, Dims d) {
+  using C = QPlan<NR, NQ>;
+  constexpr int CW = C::cw, NCH = C::nch, ST = C::st, NA = C::na, OB = C::ob;
+  extern __shared__ __align__(1024) char sm[];
+  // the finish kernel may be scheduled now; it waits for this grid's
+  // completion before it reads a partial
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (su32(sm) & 1023u) {  // (the swizzled tiles; dynamic shared memory starts at 1 KB)
+    if (threadIdx.x == 0) atomicCAS(status, 0, LOSA_ERR_DEVICE_BOUNDS);
+    return;
+  }
+  char* qs = sm;                              // NQ parts of [NR][128 B]
+  char* wbuf = qs + C::qbytes;                // [2] W buffers: [2 (W, remainder)][atoms][128][128 B]
+  char* kring = wbuf + 2 * C::wbytes;         // ST K tiles
+  char* vring = kring + ST * kTileBytes;      // ST V tiles
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vring + ST * kTileBytes);
+  uint64_t* bQ = bars;           // query parts staged (8 warps)
+  uint64_t* bS = bars + 1;       // [2] S^T and the info of an even / odd tile ready (MMA, scales)
+  uint64_t* bO = bars + 3;       // [2] O = V W of an even / odd tile done
+  uint64_t* bP = bars + 5;       // [2] W and V^T of an even / odd tile written (8 + 4 warps)
+  uint64_t* bKf = bars + 7;      // [ST] K tile landed
+  uint64_t* bKe = bKf + ST;      // [ST] its MMAs done
+  uint64_t* bVf = bKe + ST;      // [ST] V tile landed
+  uint64_t* bVe = bVf + ST;      // [ST] read (4 warps)
+  float* rf = reinterpret_cast<float*>(bars + C::nbars + 1);  // [NR] 2^-c: undoes a row's scaling
+  float* nm = rf + NR;           // [NR] minus the row's reference (+inf: none yet)
+  float* xch = nm + NR;          // [2][4][32] warp maxima / sums of a warp group
+  float* alpha = xch + 256;      // [2][32] factors of a moved reference
+  TileInfo* info = reinterpret_cast<TileInfo*>(alpha + 64);  // [2]
+  int* line = reinterpret_cast<int*>(info + 2);  // tiles of this CTA, then s, g, lt of the first
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(line + 4);
+  int* s_fail = reinterpret_cast<int*>(tslot + 1);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rows = d.G * d.B, r0 = blockIdx.y * NR, nrows = min(NR, rows - r0);
+
+  if (warp == 0) {
+    // this CTA's range of the line, and where it starts
+    long long before, all;
+    line_sums(d, 0, before, all);
+    const long long total = all * d.Hkv;
+    const int n = line_ctas_used(d, total), b = blockIdx.x;
+    const long long x0 = b < n ? b * total / n : 0, x1 = b < n ? (b + 1) * total / n : 0;
+    int s = 0;
+    before = 0;
+    if (d.lens) {
+      bool found = false;
+      for (int s0 = 0; s0 < d.S && !found; s0 += 32) {
+        const int i = s0 + lane;
+        int incl = i < d.S ? line_tiles(d, i) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, (before + incl) * d.Hkv > x0);
+        found = past != 0;
+        const int at = found ? __ffs(past) - 1 : 31;
+        const int upto = __shfl_sync(0xffffffffu, incl, at > 0 ? at - 1 : 0);
+        const int last = __shfl_sync(0xffffffffu, incl, 31);
+        s = s0 + at;
+        before += found ? (at > 0 ? upto : 0) : last;
+      }
+    } else {
+      const long long nt = (d.L + kLineKeys - 1) / kLineKeys;
+      s = static_cast<int>(x0 / (nt * d.Hkv));
+      before = nt * s;
+    }
+    if (lane == 0) {
+      const long long nt = line_tiles(d, s), y = x0 - before * d.Hkv;
+      line[0] = static_cast<int>(x1 - x0);
+      line[1] = s;
+      line[2] = static_cast<int>(y / nt);
+      line[3] = static_cast<int>(y % nt);
+      for (int i = 0; i < C::nbars; ++i)
+        mbar_init(&bars[i], i == 0 ? 8 : i < 3 ? 2 : i < 5 ? 1 : i < 7 ? 12 : i >= 7 + 3 * ST ? 4 : 1);
+      fence_mbar_init();
+      *s_fail = 0;
+    }
+    if (b == 0 && blockIdx.y == 0)
+      for (int i = lane; d.lens && i < d.S; i += 32)
+        if (seq_len_bad(d, i)) atomicCAS(status, 0, LOSA_ERR_DEVICE_BOUNDS);
+    __syncwarp();
+    tmem_alloc(tslot, C::cols);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = __shfl_sync(0xffffffffu, *tslot, 0);
+  const int n = __shfl_sync(0xffffffffu, line[0], 0);  // this CTA's tiles
+  LinePos pos;
+  pos.s = __shfl_sync(0xffffffffu, line[1], 0);
+  pos.g = __shfl_sync(0xffffffffu, line[2], 0);
+  pos.lt = __shfl_sync(0xffffffffu, line[3], 0);
+  pos.start(d);
+  bool ok = true;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 12 && n > 0) {
+      // ---- loads: K and V tiles through rings of ST stages, one thread
+      if (lane == 0) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+        int it = 0;
+#pragma unroll 1
+        for (; it < n && ok; ++it) {
+          const int st = it % ST, use = it / ST;
+          const int row = (pos.s * d.Hkv + pos.g) * d.Lc + pos.lt * kLineKeys;
+          if (use > 0) ok = mbar_wait(&bKe[st], (use - 1) & 1);
+          if (!ok) break;
+          mbar_expect_tx(&bKf[st], kTileBytes);
+          tma_load_2d(kring + st * kTileBytes, &kmap, 0, row, &bKf[st]);
+          if (use > 0) ok = mbar_wait(&bVe[st], (use - 1) & 1);
+          if (!ok) break;
+          mbar_expect_tx(&bVf[st], kTileBytes);
+          tma_load_2d(vring + st * kTileBytes, &vmap, 0, row, &bVf[st]);
+          pos.next(d);
+        }
+        if (!ok) {
+          // the copies in flight land before the CTA's shared memory goes (each
+          // stage's last one is its latest phase; tile it's K copy may be out)
+          *s_fail = 1;
+          for (int j = max(0, it - ST); j < it; ++j) {
+            mbar_wait(&bKf[j % ST], (j / ST) & 1);
+            mbar_wait(&bVf[j % ST], (j / ST) & 1);
+          }
+          if (it < n) mbar_wait(&bKf[it % ST], (it / ST) & 1);
+        }
+      }
+    } else if (warp == 13 && n > 0) {
+      // ---- MMAs: the whole warp follows the loop (so that descriptors stay in
+      // uniform registers), one elected thread issues
+      constexpr uint32_t idS = umma_idesc_e4m3(128, NR), idO = umma_idesc_f16_bmn(128, NR);
+      const bool me = elect_one();
+      const uint64_t dq = umma_desc(su32(qs), 16, 1024);
+      const uint64_t dk0 = umma_desc(su32(kring), 16, 1024);
+      const uint64_t dw0 = umma_desc(su32(wbuf), C::atom, 1024);
+      int seg = 0;  // query tiles staged so far
+      auto issue_s = [&](int it, bool fresh) {  // S^T of tile it
+        const int st = it % ST;
+        if (fresh) {
+          ok = ok && mbar_wait(bQ, seg & 1);
+          ++seg;
+        }
+        ok = ok && mbar_wait(&bKf[st], (it / ST) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        tc_fence_after();
+        const uint64_t dk = dk0 + static_cast<uint64_t>((st * kTileBytes) >> 4);
+        const uint32_t ts = tb + C::tS + (it & 1) * (NA * NR);
+        if (me) {
+          // the small parts first: the sum is truncated to its size at every step
+#pragma unroll
+          for (int a = NA - 1; a >= 0; --a)
+#pragma unroll
+            for (int p = NQ / NA - 1; p >= 0; --p)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_e4m3(ts + a * NR, dk + ((k * 32) >> 4),
+                          dq + (((a * (NQ / NA) + p) * NR * kD + k * 32) >> 4), idS,
+                          p < NQ / NA - 1 || k > 0);
+          umma_commit(&bS[it & 1]);
+          umma_commit(&bKe[st]);
+        }
+        __syncwarp();
+      };
+      issue_s(0, true);
+#pragma unroll 1
+      for (int it = 0; it < n; ++it) {
+        pos.next(d);
+        const bool more = it + 1 < n, fresh = pos.lt == 0;
+        // the next tile's scores run during this tile's softmax, unless they
+        // wait for the next KV head's queries, which are staged after it
+        if (more && !fresh) issue_s(it + 1, false);
+        ok = ok && mbar_wait(&bP[it & 1], (it >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint64_t dw = dw0 + static_cast<uint64_t>(((it & 1) * C::wbytes) >> 4);
+        const uint32_t to = tb + C::tO + (OB == 2 ? (it & 1) * NR : 0);
+        const uint32_t tv = tb + C::tV + (it & 1) * kVCols;
+        if (me) {
+#pragma unroll
+          for (int h = 1; h >= 0; --h)  // (the remainder first)
+#pragma unroll
+            for (int k = 0; k < kLineKeys / 16; ++k)
+              umma_f16_ta(to, tv + k * 8, dw + ((h * C::watoms * C::atom + k * 16 * 128) >> 4), idO,
+                          h == 0 || k > 0);
+          umma_commit(&bO[it & 1]);
+        }
+        __syncwarp();
+        if (more && fresh) issue_s(it + 1, true);
+      }
+      if (!ok) *s_fail = 1;
+    } else if (warp == 14 && n > 0) {
+      // ---- a tile's scales: lane p < 8 its page p's, read a tile ahead
+      float k_ = 1.f, v_ = 1.f;
+      auto fetch = [&]() {
+        const int j = pos.lt * kLineKeys + lane * kPS;
+        k_ = v_ = 1.f;
+        if (lane < kLineKeys / kPS && j < pos.L) {
+          const size_t i = static_cast<size_t>(pos.s * d.Hkv + pos.g) * d.Pc + (j >> 4);
+          k_ = __ldg(ks + i);
+          v_ = __ldg(vs + i);
+        }
+      };
+      fetch();
+#pragma unroll 1
+      for (int it = 0; it < n && ok; ++it) {
+        const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
+        const float v = fmaxf(v_, kMinScale);
+        const float4 w = make_float4(k_ * d.scale_log2, log2f(v), 1.f / v, 0.f);
+        pos.next(d);
+        const int last = it + 1 == n || pos.lt == 0;
+        if (it + 1 < n) fetch();
+        // (the info of two tiles back has been read)
+        if (it >= 2) ok = mbar_wait(&bP[it & 1], ((it - 2) >> 1) & 1);
+        TileInfo& t = info[it & 1];
+        if (lane < kLineKeys / kPS) t.page[lane] = w;
+        if (lane == 0) {
+          t.nv = nv;
+          t.last = last;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bS[it & 1]);
+      }
+      if (!ok) *s_fail = 1;
+    } else if (warp < 12) {
+      // ---- V codes -> fp16, transposed, into TMEM: warp w4 has the channels
+      // 32 w4 .. (its TMEM lanes)
+      const int w4 = warp & 3;
+      const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
+#pragma unroll 1
+      for (int it = 0; it < n; ++it) {
+        const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
+        ok = ok && mbar_wait(&bVf[it % ST], (it / ST) & 1);
+        const uint32_t vt = su32(vring + (it % ST) * kTileBytes);
+        uint32_t c[2][16];
+#pragma unroll
+        for (int dh = 0; dh < 2; ++dh)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = i * 16 + (lane & 15);
+            ldsm_b8_trans(vt + j * 128 + (((2 * w4 + dh) ^ (j & 7)) << 4), c[dh][2 * i],
+                          c[dh][2 * i + 1]);
+          }
+        if (nv < kLineKeys) {
+          // keys past the prefix may hold anything, and 0 times NaN is NaN
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int m = min(max(nv - (i * 16 + 4 * (lane & 3)), 0), 4);
+            const uint32_t mask = m == 4 ? 0xffffffffu : (1u << (8 * m)) - 1u;
+#pragma unroll
+            for (int dh = 0; dh < 2; ++dh) {
+              c[dh][2 * i] &= mask;
+              c[dh][2 * i + 1] &= mask;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bVe[it % ST]);
+        // V^T of this parity is free once O = V W of two tiles back is done
+        if (it >= 2) ok = ok && mbar_wait(&bO[it & 1], ((it - 2) >> 1) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int dh = 0; dh < 2; ++dh)
+#pragma unroll
+          for (int kq = 0; kq < 2; ++kq) {
+            uint32_t f[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              e4m3x4_to_f16x2(c[dh][kq * 8 + i], f[2 * i], f[2 * i + 1]);
+            tmem_st16x256_x4_raw(tb + C::tV + (it & 1) * kVCols + kq * 32 + lane_off +
+                                     (static_cast<uint32_t>(dh * 16) << 16),
+                                 f);
+          }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bP[it & 1]);
+        pos.next(d);
+      }
+      if (!ok) *s_fail = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ---- softmax warps: warp w has TMEM lanes 32 (w % 4) .., keys of the S^T
+    // tile and channels of O^T; warp group w / 4 has the query columns
+    // [ch wg, ch wg + ch)
+    const int w4 = warp & 3, wg = warp >> 2, c0 = wg * C::ch;
+    const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
+    const int key = 32 * w4 + lane;
+    u64 l[C::ch / 2], o[C::ch / 2];
+    int since = 0;  // tile of this KV head within the CTA
+    bool fresh = true;
+    uint32_t pend = 0;  // bit cc: chunk cc's O of the tile before has not been read yet
+
+    // o += the columns of O buffer b (one MMA's result: a whole tile)
+    auto take_o = [&](int cc, int b) {
+#pragma unroll
+      for (int i0 = 0; i0 < CW; i0 += (CW < 16 ? CW : 16)) {
+        float t[CW < 16 ? CW : 16];
+        tmem_ld(tb + C::tO + (OB == 2 ? b * NR : 0) + c0 + cc * CW + i0 + lane_off, t);
+#pragma unroll
+        for (int i = 0; i < (CW < 16 ? CW : 16); i += 2) {
+          u64& x = o[(cc * CW + i0 + i) / 2];
+          x = add2(x, pk(t[i], t[i + 1]));
+        }
+      }
+    };
+    // the scores of chunk cc, as 2^x and columns: S rf kf + lv
+    auto load_x = [&](int it, int cc, u64 kf2, u64 lv2, u64 (&y)[CW / 2]) {
+      const int cb = c0 + cc * CW;
+      float a[CW];
+      tmem_ld(tb + C::tS + (it & 1) * (NA * NR) + cb + lane_off, a);
+#pragma unroll
+      for (int i = 0; i < CW; i += 2) y[i / 2] = pk(a[i], a[i + 1]);
+      if (NA == 2) {
+        tmem_ld(tb + C::tS + (it & 1) * (NA * NR) + NR + cb + lane_off, a);
+        const u64 ps = pk(1.f / kPartScale, 1.f / kPartScale);
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) y[i / 2] = fma2(pk(a[i], a[i + 1]), ps, y[i / 2]);
+      }
+#pragma unroll
+      for (int i = 0; i < CW; i += 4) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(rf + cb + i);
+        y[i / 2] = fma2(mul2(y[i / 2], r.x), kf2, lv2);
+        y[i / 2 + 1] = fma2(mul2(y[i / 2 + 1], r.y), kf2, lv2);
+      }
+    };
+#pragma unroll 1
+    for (int it = 0; it < n; ++it) {
+      if (fresh) {
+        // ---- a KV head begins: its queries, in parts (the S MMAs that read
+        // the previous head's are done: this thread has waited for them)
+        since = 0;
+        pend = 0;
+#pragma unroll
+        for (int i = 0; i < C::ch / 2; ++i) l[i] = o[i] = 0ull;
+        bar_sync(3, kSoftmaxThreads);
+        const size_t q0 = ((static_cast<size_t>(pos.s) * d.Hq + pos.g * d.G) * d.B + r0) * kD;
+#pragma unroll 1
+        for (int r = warp; r < NR; r += 8) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < nrows) x = ld4(Q, q0 + static_cast<size_t>(r) * kD + 4 * lane, d.dtype);
+          const float amax = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+          const int c = 7 - max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -119);
+          const float sc = exp2_int(c);
+          x = make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+          char* dst = qs + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+          for (int p = 0; p < NQ; ++p) {
+            // (an infinite row maximum leaves no number: NaN, as its softmax)
+            const uint32_t w = amax < INFINITY ? e4m3x4(x.x, x.y, x.z, x.w) : 0x7f7f7f7fu;
+            *reinterpret_cast<uint32_t*>(dst + p * NR * kD) = w;
+            const float4 y = e4m3x4_to_f32(w);
+            const float f = NA == 2 && p == NQ / 2 - 1 ? kPartScale : 1.f;
+            x = make_float4((x.x - y.x) * f, (x.y - y.y) * f, (x.z - y.z) * f, (x.w - y.w) * f);
+          }
+          if (lane == 0) {
+            rf[r] = amax < INFINITY ? exp2_int(-c) : 1.f;
+            nm[r] = INFINITY;
+          }
+        }
+        fence_async_smem();
+        bar_sync(3, kSoftmaxThreads);
+        if (lane == 0) mbar_arrive(bQ);
+      }
+      // S^T of this tile and all MMAs issued before it are done: O = V W of two
+      // tiles back too, so W's buffer of this parity is free
+      ok = ok && mbar_wait(&bS[it & 1], (it >> 1) & 1);
+      tc_fence_after();
+      const TileInfo& ti = info[it & 1];
+      const int nv = ti.nv;
+      const bool last = ti.last;
+      const float4 pg = ti.page[key >> 4];
+      const bool valid = key < nv;
+      const u64 kf2 = pk(pg.x, pg.x), lv2 = pk(pg.y, pg.y);
+      const float rv = valid ? pg.z : 0.f;
+      const u64 rv2 = pk(rv, rv);
+      char* wb = wbuf + (it & 1) * C::wbytes;
+#pragma unroll
+      for (int cc = 0; cc < NCH; ++cc) {
+        const int cb = c0 + cc * CW;  // first column
+        u64 y[CW / 2];
+        load_x(it, cc, kf2, lv2, y);
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < CW; i += 4) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + cb + i);
+          y[i / 2] = add2(y[i / 2], m.x);
+          y[i / 2 + 1] = add2(y[i / 2 + 1], m.y);
+          const float2 a = up(y[i / 2]), b = up(y[i / 2 + 1]);
+          top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+        }
+        if (OB == 2 && since >= 2) {
+          // O of two tiles back (unless a moved reference has taken it already)
+          if (pend & (2u << (2 * cc))) take_o(cc, it & 1);
+        }
+        pend = (pend & ~(2u << (2 * cc))) | ((pend & (1u << (2 * cc))) << 1);
+        if (bar_or(1 + wg, 128, valid && top > kRefMove)) {
+          // ---- some row's reference moves (the first tile; then seldom): the
+          // columns' maxima over the tile's keys, references, and what has been
+          // accumulated against the old ones
+          load_x(it, cc, kf2, lv2, y);
+          float mine = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < CW; i += 2) {
+            const float2 a = up(y[i / 2]);
+            const float m0 = redux_max(valid ? a.x : -INFINITY);
+            const float m1 = redux_max(valid ? a.y : -INFINITY);
+            if (lane == i) mine = m0;
+            if (lane == i + 1) mine = m1;
+          }
+          if (lane < CW) xch[(wg * 4 + w4) * 32 + lane] = mine;
+          bar_sync(1 + wg, 128);
+          if (w4 == 0 && lane < CW) {
+            float m = mine;
+#pragma unroll
+            for (int w = 1; w < 4; ++w) m = fmaxf(m, xch[(wg * 4 + w) * 32 + lane]);
+            const float old = -nm[cb + lane];
+            const bool move = m > old + kRefMove || (old == -INFINITY && m > old);
+            const float ref = move ? m - kRefTop : old;
+            alpha[wg * 32 + lane] = move ? exp2f(old - ref) : 1.f;
+            nm[cb + lane] = -ref;
+          }
+          bar_sync(1 + wg, 128);
+          if (since > 0) {
+            if (pend & (2u << (2 * cc))) {  // the tile before's
+              ok = ok && mbar_wait(&bO[(it - 1) & 1], ((it - 1) >> 1) & 1);
+              tc_fence_after();
+              take_o(cc, (it - 1) & 1);
+              pend &= ~(2u << (2 * cc));
+            }
+#pragma unroll
+            for (int i = 0; i < CW; i += 2) {
+              const u64 a = *reinterpret_cast<const u64*>(alpha + wg * 32 + i);
+              o[(cc * CW + i) / 2] = mul2(o[(cc * CW + i) / 2], a);
+              l[(cc * CW + i) / 2] = mul2(l[(cc * CW + i) / 2], a);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < CW; i += 2)
+            y[i / 2] = add2(y[i / 2], *reinterpret_cast<const u64*>(nm + cb + i));
+          // (the next vote's slow path writes xch, nm and alpha only after a
+          // barrier of this warp group)
+        }
+        if (nv < kLineKeys) {
+          const u64 none = pk(-INFINITY, -INFINITY);
+#pragma unroll
+          for (int i = 0; i < CW / 2; ++i) y[i] = valid ? y[i] : none;
+        }
+#pragma unroll
+        for (int i = 0; i < CW; i += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 a = up(y[i / 2 + u]);
+            const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            const u64 w2 = pk(w.x, w.y);
+            u64& lx = l[(cc * CW + i) / 2 + u];
+            lx = fma2(w2, rv2, lx);
+            hi[u] = pack_f16x2(w.x, w.y);
+            const float2 f = f16x2_to_f32(hi[u]);
+            const float2 r = up(fma2(pk(f.x, f.y), pk(-1.f, -1.f), w2));
+            lo[u] = pack_f16x2(r.x, r.y);
+          }
+          const int col = cb + i;  // its 16-byte chunk of the key's row
+          char* dst = wb + (col >> 6) * C::atom + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + C::watoms * C::atom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (OB == 1 && since > 0 && (pend & (2u << (2 * cc)))) {
+          // one O buffer: the tile before's result, before this tile's MMA
+          if (cc == 0) ok = ok && mbar_wait(&bO[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          tc_fence_after();
+          take_o(cc, 0);
+          pend &= ~(2u << (2 * cc));
+        }
+        pend |= 1u << (2 * cc);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bP[it & 1]);
+      ++since;
+      fresh = last;
+
+      if (last) {
+        // ---- the KV head ends here: the partial of its rows
+        ok = ok && mbar_wait(&bO[it & 1], (it >> 1) & 1);  // (in order: the tile before's too)
+        tc_fence_after();
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) *s_fail = 1;
+        const int sg = pos.s * d.Hkv + pos.g;
+        float* dst0 = part + ((static_cast<size_t>(blockIdx.x) + sg) * rows + r0) * kPartStride;
+#pragma unroll
+        for (int cc = 0; cc < NCH; ++cc) {
+          const int cb = c0 + cc * CW;
+          if (OB == 2 && (pend & (2u << (2 * cc)))) take_o(cc, (it - 1) & 1);
+          take_o(cc, it & 1);
+          // sums over the lanes: after the exchange of halves, lane i / (32 / CW)
+          // holds column i's
+          float v[CW];
+#pragma unroll
+          for (int i = 0; i < CW; i += 2) {
+            const float2 a = up(l[(cc * CW + i) / 2]);
+            v[i] = a.x;
+            v[i + 1] = a.y;
+          }
+          int w = CW;
+#pragma unroll
+          for (int sh = 16; sh > 0; sh >>= 1) {
+            if (w > 1) {
+              w >>= 1;
+              const bool hi = lane & sh;
+#pragma unroll
+              for (int i = 0; i < CW / 2; ++i) {
+                if (i < w) {
+                  const float send = hi ? v[i] : v[i + w], keep = hi ? v[i + w] : v[i];
+                  v[i] = keep + __shfl_xor_sync(0xffffffffu, send, sh);
+                }
+              }
+            } else {
+              v[0] += __shfl_xor_sync(0xffffffffu, v[0], sh);
+            }
+          }
+          bar_sync(1 + wg, 128);  // (xch: the maxima, or the chunk before, have been read)
+          if (lane % (32 / CW) == 0) xch[(wg * 4 + w4) * 32 + lane / (32 / CW)] = v[0];
+          bar_sync(1 + wg, 128);
+          const bool good = *s_fail == 0;
+#pragma unroll
+          for (int i = 0; i < CW; i += 2) {
+            const float2 a = up(o[(cc * CW + i) / 2]);
+            if (good && cb + i < nrows) dst0[(cb + i) * kPartStride + 4 + key] = a.x;
+            if (good && cb + i + 1 < nrows) dst0[(cb + i + 1) * kPartStride + 4 + key] = a.y;
+          }
+          if (good && w4 == 0 && lane < CW && cb + lane < nrows) {
+            float sum = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum += xch[(wg * 4 + q) * 32 + lane];
+            float* dst = dst0 + (cb + lane) * kPartStride;
+            dst[0] = -nm[cb + lane];
+            dst[1] = sum;
+          }
+        }
+        pos.next_head(d);
+      }
+    }
+    if (!__all_sync(0xffffffffu, ok) && lane == 0) *s_fail = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *s_fail) atomicCAS(status, 0, LOSA_ERR_DEVICE_TIMEOUT);
+  if (warp == 0) tmem_dealloc(tb, C::cols);
+}
+
+template <int NR, int NQ>
+int launch_partials(const Dims& d, const void* q, const void* k8, const void* v8,
+                    const float* k_scale, const float* v_scale, float* part, int* status,
+                    cudaStream_t st) {
+  using C = QPlan<NR, NQ>;
+  auto* fn = dense_quant_kernel<NR, NQ>;
+  static bool attr_done[kMaxDevices] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= kMaxDevices || !attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    if (dev >= 0 && dev < kMaxDevices) attr_done[dev] = true;
+  }
+  CUtensorMap kmap, vmap;
+  const unsigned long long nrows = static_cast<unsigned long long>(d.S) * d.Hkv * d.Lc;
+  if (make_byte_tmap(&kmap, k8, nrows, kLineKeys) != LOSA_OK ||
+      make_byte_tmap(&vmap, v8, nrows, kLineKeys) != LOSA_OK)
+    return record_cuda_error(cudaErrorInvalidValue);
+  fn<<<dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR), kThreadsQ, C::smem, st>>>(
+      q, kmap, vmap, k_scale, v_scale, part, status, d);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
 }
 
 }  // namespace
@@ -111,15 +758,18 @@ extern "C" int losa_dense_prefix_quant(const losa_shape* shape, const void* q, c
                         {out, ob, true},      {out_lse, lb, true},   {workspace, d.total, true}};
   if (any_write_alias(reg, static_cast<int>(sizeof(reg) / sizeof(reg[0]))))
     return LOSA_ERR_INVALID_ARG;
-  if (SG > 65535) return LOSA_ERR_UNSUPPORTED;
+  // (the tensor maps' row coordinate is an int)
+  if (SG > 65535 || SG * d.Lc > 0x7fffffffu) return LOSA_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.off_part);
   int* status = reinterpret_cast<int*>(static_cast<char*>(workspace) + d.off_status);
-  dense_quant_partial_kernel<<<dim3(d.nsplit, static_cast<unsigned>(SG)), kWarpsQ * 32, 0, st>>>(
-      q, static_cast<const uint8_t*>(k8), static_cast<const uint8_t*>(v8), k_scale, v_scale, part,
-      status, d);
-  rc = launch_dense_finish(d, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, st);
+  const int r = d.G * d.B;
+  auto* launch = d.dtype == LOSA_BF16 ? (r <= 16   ? launch_partials<16, 2>
+                                         : r <= 32 ? launch_partials<32, 2>
+                                         : r <= 64 ? launch_partials<64, 2>
+                                                   : launch_partials<128, 2>)
+                                      : (r <= 16 ? launch_partials<16, 6> : launch_partials<64, 6>);
+  rc = launch(d, q, k8, v8, k_scale, v_scale, part, status, st);
   if (rc != LOSA_OK) return rc;
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
+  return launch_dense_finish(d, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, st);
 }

@@ -38,6 +38,9 @@ struct Dims {
   float scale_log2;       // scale * log2(e): scores in base-2 units
   // prefix splits (dense pass)
   int nsplit, split_pages;
+  // dense pass over an 8-bit prefix: CTAs that share the line of all key tiles
+  // (below); 0: fixed splits
+  int line_ctas;
   // workspace byte offsets
   size_t off_status, off_part, total;
 };
@@ -130,6 +133,45 @@ __device__ __forceinline__ int seq_len(const Dims& d, int s) {
 // The entry of sequence s lies outside [1, L] (seq_len clamped it).
 __device__ __forceinline__ bool seq_len_bad(const Dims& d, int s) {
   return d.lens && (d.lens[s] < 1 || d.lens[s] > d.L);
+}
+
+// ---------------------------------------------------------------------------
+// The line of key tiles (dense pass over an 8-bit prefix): all 128-key tiles of
+// every (sequence, KV head), in the order s, g, tile, cut into line_ctas equal
+// ranges, one per CTA.  A CTA's range may cross from one KV head into the next;
+// it then writes a partial for each.  Walking along the line, either the CTA or
+// the KV head steps on, never both without a tile between, so c + sg numbers
+// the partials: group sg's are those of CTAs c0(sg) .. c1(sg), consecutive.
+// ---------------------------------------------------------------------------
+constexpr int kLineKeys = 128;
+__device__ __forceinline__ int line_tiles(const Dims& d, int s) {
+  return (seq_len(d, s) + kLineKeys - 1) / kLineKeys;
+}
+// Tiles of one KV head over the sequences before s, and over all sequences
+// (a whole warp calls it).
+__device__ __forceinline__ void line_sums(const Dims& d, int s, long long& before,
+                                          long long& all) {
+  const int lane = threadIdx.x & 31;
+  if (!d.lens) {
+    const long long nt = (d.L + kLineKeys - 1) / kLineKeys;
+    before = nt * s;
+    all = nt * d.S;
+    return;
+  }
+  before = all = 0;
+  for (int s0 = 0; s0 < d.S; s0 += 32) {
+    const int i = s0 + lane;
+    const int nt = i < d.S ? line_tiles(d, i) : 0;
+    all += __reduce_add_sync(0xffffffffu, nt);
+    before += __reduce_add_sync(0xffffffffu, i < s ? nt : 0);
+  }
+}
+// CTAs in use and the CTA whose range holds tile x: ranges [b T / n, (b+1) T / n).
+__device__ __forceinline__ int line_ctas_used(const Dims& d, long long total) {
+  return static_cast<int>(total < d.line_ctas ? total : d.line_ctas);
+}
+__device__ __forceinline__ int line_cta_of(long long x, long long total, int n) {
+  return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
 __device__ __forceinline__ void set_status(void* ws, int code) {
@@ -259,6 +301,11 @@ inline bool any_write_alias(const Region* r, int n) {
 }
 
 int make_dims(const losa_shape* sh, int which, Dims* d);
+// Row halves of the dense pass over an 8-bit prefix: fp32 queries take six
+// e4m3 parts each, and 128 rows of them do not fit beside the rest.
+inline int dense_quant_halves(const Dims& d) {
+  return d.dtype == LOSA_F32 && d.G * d.B > 64 ? 2 : 1;
+}
 // Whether the fused step kernel's shared-memory plan fits in `max_dyn` bytes.
 bool fused_step_fits(const Dims& d, int max_dyn);
 // Dynamic shared memory a B200 CTA may opt in to (227 KB).
@@ -287,6 +334,9 @@ int make_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsi
 // the 128-byte swizzle (the layout of two 2-D boxes at offsets 0 and
 // kPS * 128).  LOSA_ERR_CUDA if the driver refuses the map.
 int make_page_tmap(CUtensorMap* map, const void* base, unsigned long long nrows);
+// 2-D tensor map over [nrows][kD] bytes, 128-byte-swizzled boxes of whole rows
+// x box_rows.
+int make_byte_tmap(CUtensorMap* map, const void* base, unsigned long long nrows, unsigned box_rows);
 int num_sms();
 
 }  // namespace losa
