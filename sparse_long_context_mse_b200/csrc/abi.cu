@@ -143,10 +143,20 @@ int make_dims(const losa_shape* sh, int which, Dims* d) {
   d->off_status = off;
   off += 256;
   if (which == LOSA_WS_DENSE_QUANT) {
-    // one CTA per SM, or two for the two halves of more than 64 fp32 rows
+    // one CTA per SM, two of them for each range when there are over 64 rows
     const int halves = dense_quant_halves(*d);
     const long long tiles = (d->L + kLineKeys - 1) / kLineKeys * static_cast<long long>(SG);
     d->line_ctas = static_cast<int>(std::min<long long>(kSizingSms / halves, tiles));
+    // A CTA that crosses from one KV head into the next loses about four tiles'
+    // time (its pipeline drains, the next queries are staged).  Sequences of one
+    // length can be cut at KV heads, with a whole number of CTAs for each: better
+    // while the longest range grows by less than that.
+    const long long per = d->line_ctas / static_cast<long long>(SG);
+    if (!d->lens && per > 0) {
+      const long long nt = tiles / static_cast<long long>(SG);
+      const long long cut = (nt + per - 1) / per, line = (tiles + d->line_ctas - 1) / d->line_ctas;
+      if (cut < line + 4) d->line_ctas = static_cast<int>(per * SG);
+    }
     d->off_part = off;
     off += align256((SG + d->line_ctas - 1) * static_cast<size_t>(G * d->B) * kPartStride *
                     sizeof(float));

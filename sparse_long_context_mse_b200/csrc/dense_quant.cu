@@ -15,8 +15,8 @@
 // laid out so that nothing on the chip takes longer:
 //
 // * Keys are the rows of both products (M = 128, one tile), the G*B query rows
-//   are the columns (N = 16 .. 128): few query rows cost little, one decoded
-//   token as well as a block of 32.
+//   are the columns (N = 16, 32 or 64; 128 rows take two CTAs that read the same
+//   keys at the same time, the second time from L2): few query rows cost little.
 // * S^T = K8 Q^T runs on the codes as TMA brought them (kind::f8f6f4, e4m3 times
 //   e4m3): nothing converts K.  Q enters as a sum of e4m3 parts, each the
 //   rounding of what the parts before it left: a bf16 number has 8 significant
@@ -47,13 +47,9 @@
 namespace losa {
 namespace {
 
-// Warps 0-7: softmax; 8-11: V to fp16; 12 loads, 13 issues MMAs, 14 prepares the
-// tiles' scales, 15 has nothing to do.  The first two warp groups take registers
-// over from the other two: 256 x 192 + 256 x 64 = the launch's 512 x 128.
-constexpr int kSoftmaxThreads = 256;
-constexpr int kThreadsQ = 512;
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
-static_assert(256 * (kSoftmaxRegs + kOtherRegs) == kThreadsQ * 128, "register split");
+// Softmax warp groups first (2, or 4 for 64 columns), then four warps that widen
+// V, then one that loads, one that issues MMAs, one that prepares the tiles'
+// scales and one that has nothing to do.
 constexpr int kTileBytes = kLineKeys * kD;  // one K or V tile of codes: 16 KB
 constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (fp16 pairs)
 constexpr float kRefTop = 11.f;             // a new reference puts the row's maximum at 2^11 ..
@@ -92,33 +88,38 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
 // NR: query columns (MMA N); NQ: e4m3 parts of a query row (2: bf16, 6: fp32).
 template <int NR, int NQ>
 struct QPlan {
-  static constexpr int ch = NR / 2;                      // columns per softmax warp group
-  static constexpr int cw = ch < 32 ? ch : 32;           // columns handled at a time
-  static constexpr int nch = ch / cw;
+  // A tile takes a softmax warp a chain of some 60 dependent waits and
+  // instructions per column, so the columns are spread over as many warps as the
+  // registers allow: 16 columns per thread at most.
+  static constexpr int nwg = NR > 32 ? 4 : 2;            // softmax warp groups
+  static constexpr int soft = nwg * 128;                 // .. threads
+  static constexpr int threads = soft + 256;
+  // the softmax warps take registers over from the others
+  static constexpr int regs = nwg == 4 ? 80 : 128;       // at launch
+  static constexpr int soft_regs = nwg == 4 ? 96 : 192, other_regs = nwg == 4 ? 48 : 64;
+  static_assert(soft * soft_regs + 256 * other_regs <= threads * regs, "register split");
+  static constexpr int cw = NR / nwg;                    // columns per softmax warp group
   static constexpr int na = NQ > 3 ? 2 : 1;              // score accumulators
-  static constexpr int ob = NR > 64 ? 1 : 2;             // O buffers
   static constexpr int atom = kLineKeys * 128;           // 64 fp16 columns of W: 16 KB
-  static constexpr int watoms = NR > 64 ? 2 : 1;
-  static constexpr int wbytes = 2 * watoms * atom;       // W and its remainder
+  static constexpr int wbytes = 2 * atom;                // W and its remainder
   static constexpr int qbytes = NQ * NR * kD;
   static constexpr int small = 3072;                     // barriers, row factors, exchange
   static constexpr int room = kB200MaxDynSmem - small - qbytes - 2 * wbytes;
   static constexpr int st = room / (2 * kTileBytes) < 4 ? room / (2 * kTileBytes) : 4;
   static constexpr int nbars = 7 + 4 * st;
   static constexpr int smem = qbytes + 2 * wbytes + 2 * st * kTileBytes + small;
-  static constexpr uint32_t tS = 0, tO = 2 * na * NR, tV = tO + ob * NR, cols = 512;
-  static_assert(st >= 2 && smem <= kB200MaxDynSmem, "shared memory");
+  static constexpr uint32_t tS = 0, tO = 2 * na * NR, tV = tO + 2 * NR, cols = 512;
+  static_assert(NR <= 64 && st >= 2 && smem <= kB200MaxDynSmem, "shared memory");
   static_assert(tV + 2 * kVCols <= 512, "TMEM");
-  static_assert(nbars * 8 + 8 + 2 * NR * 4 + 2 * 4 * 32 * 4 + 2 * 32 * 4 + 2 * 144 + 64 <= small,
+  static_assert(nbars * 8 + 8 + 7 * NR * 4 + 2 * 128 + 64 <= small,
                 "small area");
 };
 
 // What the softmax warps have to know of a tile.
 struct __align__(16) TileInfo {
-  float4 page[kLineKeys / kPS];  // score factor, log2 and reciprocal of the value scale
-  int nv;                        // real keys
-  int last;                      // the KV head's last tile in this CTA
-  int pad[2];
+  // a page's score factor, log2 and reciprocal of the value scale; and, in every
+  // entry, the tile's real keys, + 256 if it is the KV head's last in this CTA
+  float4 page[kLineKeys / kPS];
 };
 
 // A CTA's place on the line of tiles.
@@ -139,21 +140,14 @@ struct LinePos {
   }
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
-}
-
 template <int NR, int NQ>
-__global__ void __launch_bounds__(kThreadsQ, 1)
+__global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
     dense_quant_kernel(const void* __restrict__ Q, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const float* __restrict__ ks,
                        const float* __restrict__ vs, float* __restrict__ part,
                        int* __restrict__ status, Dims d) {
   using C = QPlan<NR, NQ>;
-  constexpr int CW = C::cw, NCH = C::nch, ST = C::st, NA = C::na, OB = C::ob;
+  constexpr int CW = C::cw, ST = C::st, NA = C::na, NS = C::soft, W0 = NS / 32;
   extern __shared__ __align__(1024) char sm[];
   // the finish kernel may be scheduled now; it waits for this grid's
   // completion before it reads a partial
@@ -163,23 +157,23 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
     return;
   }
   char* qs = sm;                              // NQ parts of [NR][128 B]
-  char* wbuf = qs + C::qbytes;                // [2] W buffers: [2 (W, remainder)][atoms][128][128 B]
+  char* wbuf = qs + C::qbytes;                // [2] W buffers: [2 (W, remainder)][128][128 B]
   char* kring = wbuf + 2 * C::wbytes;         // ST K tiles
   char* vring = kring + ST * kTileBytes;      // ST V tiles
   uint64_t* bars = reinterpret_cast<uint64_t*>(vring + ST * kTileBytes);
-  uint64_t* bQ = bars;           // query parts staged (8 warps)
-  uint64_t* bS = bars + 1;       // [2] S^T and the info of an even / odd tile ready (MMA, scales)
-  uint64_t* bO = bars + 3;       // [2] O = V W of an even / odd tile done
-  uint64_t* bP = bars + 5;       // [2] W and V^T of an even / odd tile written (8 + 4 warps)
+  uint64_t* bS = bars;           // [2] S^T and the info of an even / odd tile ready (MMA, scales)
+  uint64_t* bO = bars + 2;       // [2] O = V W of an even / odd tile done
+  uint64_t* bP = bars + 4;       // [2] W and V^T of an even / odd tile written (softmax and V warps)
+  uint64_t* bQ = bars + 6;       // query parts staged (softmax warps)
   uint64_t* bKf = bars + 7;      // [ST] K tile landed
   uint64_t* bKe = bKf + ST;      // [ST] its MMAs done
   uint64_t* bVf = bKe + ST;      // [ST] V tile landed
   uint64_t* bVe = bVf + ST;      // [ST] read (4 warps)
   float* rf = reinterpret_cast<float*>(bars + C::nbars + 1);  // [NR] 2^-c: undoes a row's scaling
   float* nm = rf + NR;           // [NR] minus the row's reference (+inf: none yet)
-  float* xch = nm + NR;          // [2][4][32] warp maxima / sums of a warp group
-  float* alpha = xch + 256;      // [2][32] factors of a moved reference
-  TileInfo* info = reinterpret_cast<TileInfo*>(alpha + 64);  // [2]
+  float* xch = nm + NR;          // [warp groups][4][columns] warp maxima / sums
+  float* alpha = xch + 4 * NR;   // [NR] factors of a moved reference
+  TileInfo* info = reinterpret_cast<TileInfo*>(alpha + NR);  // [2]
   int* line = reinterpret_cast<int*>(info + 2);  // tiles of this CTA, then s, g, lt of the first
   uint32_t* tslot = reinterpret_cast<uint32_t*>(line + 4);
   int* s_fail = reinterpret_cast<int*>(tslot + 1);
@@ -225,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       line[2] = static_cast<int>(y / nt);
       line[3] = static_cast<int>(y % nt);
       for (int i = 0; i < C::nbars; ++i)
-        mbar_init(&bars[i], i == 0 ? 8 : i < 3 ? 2 : i < 5 ? 1 : i < 7 ? 12 : i >= 7 + 3 * ST ? 4 : 1);
+        mbar_init(&bars[i], i < 2 ? 2 : i < 4 ? 1 : i < 6 ? W0 + 4 : i == 6 ? W0 : i >= 7 + 3 * ST ? 4 : 1);
       fence_mbar_init();
       *s_fail = 0;
     }
@@ -245,18 +239,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
   pos.g = __shfl_sync(0xffffffffu, line[2], 0);
   pos.lt = __shfl_sync(0xffffffffu, line[3], 0);
   pos.start(d);
-  bool ok = true;
-
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 12 && n > 0) {
+  if (warp >= W0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::other_regs));
+    if (warp == W0 + 4 && n > 0) {
       // ---- loads: K and V tiles through rings of ST stages, one thread
       if (lane == 0) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
         int it = 0;
+        bool ok = true;
 #pragma unroll 1
-        for (; it < n && ok; ++it) {
+        for (; it < n; ++it) {
           const int st = it % ST, use = it / ST;
           const int row = (pos.s * d.Hkv + pos.g) * d.Lc + pos.lt * kLineKeys;
           if (use > 0) ok = mbar_wait(&bKe[st], (use - 1) & 1);
@@ -277,73 +270,80 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
             mbar_wait(&bKf[j % ST], (j / ST) & 1);
             mbar_wait(&bVf[j % ST], (j / ST) & 1);
           }
-          if (it < n) mbar_wait(&bKf[it % ST], (it / ST) & 1);
+          mbar_wait(&bKf[it % ST], (it / ST) & 1);
         }
       }
-    } else if (warp == 13 && n > 0) {
-      // ---- MMAs: the whole warp follows the loop (so that descriptors stay in
-      // uniform registers), one elected thread issues
-      constexpr uint32_t idS = umma_idesc_e4m3(128, NR), idO = umma_idesc_f16_bmn(128, NR);
-      const bool me = elect_one();
-      const uint64_t dq = umma_desc(su32(qs), 16, 1024);
-      const uint64_t dk0 = umma_desc(su32(kring), 16, 1024);
-      const uint64_t dw0 = umma_desc(su32(wbuf), C::atom, 1024);
+    } else if (warp == W0 + 5 && n > 0) {
+      // ---- MMAs: the whole warp follows the loop, one elected thread issues
+      constexpr uint32_t idS = umma_idesc_e4m3(128, NR);
+      constexpr uint32_t idO = umma_idesc_f16_bmn(128, NR);
+      constexpr uint32_t idR = idO | (1u << 14);  // minus B: the remainder is stored negated
+      const uint64_t dq = umma_desc(su32(qs), 16, 1024), dk = umma_desc(su32(kring), 16, 1024);
+      const uint64_t dw = umma_desc(su32(wbuf), C::atom, 1024);
+      const uint32_t q_lo = desc_lo(dq), k_lo = desc_lo(dk), kq_hi = desc_hi(dq);
+      const uint32_t w_lo = desc_lo(dw), w_hi = desc_hi(dw);
       int seg = 0;  // query tiles staged so far
-      auto issue_s = [&](int it, bool fresh) {  // S^T of tile it
-        const int st = it % ST;
+      int ks_ = 0, kph = 0;  // K stage and phase of the next S^T
+      auto issue_s = [&](int par, bool fresh) {  // the next S^T, into buffer par
         if (fresh) {
-          ok = ok && mbar_wait(bQ, seg & 1);
+          mbar_wait_or(bQ, seg & 1, s_fail);
           ++seg;
         }
-        ok = ok && mbar_wait(&bKf[st], (it / ST) & 1);
-        if (!__all_sync(0xffffffffu, ok)) return;
-        tc_fence_after();
-        const uint64_t dk = dk0 + static_cast<uint64_t>((st * kTileBytes) >> 4);
-        const uint32_t ts = tb + C::tS + (it & 1) * (NA * NR);
-        if (me) {
-          // the small parts first: the sum is truncated to its size at every step
-#pragma unroll
-          for (int a = NA - 1; a >= 0; --a)
-#pragma unroll
-            for (int p = NQ / NA - 1; p >= 0; --p)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_e4m3(ts + a * NR, dk + ((k * 32) >> 4),
-                          dq + (((a * (NQ / NA) + p) * NR * kD + k * 32) >> 4), idS,
-                          p < NQ / NA - 1 || k > 0);
-          umma_commit(&bS[it & 1]);
-          umma_commit(&bKe[st]);
-        }
+        mbar_wait_or(&bKf[ks_], kph, s_fail);
         __syncwarp();
+        tc_fence_after();
+        const uint32_t kl = k_lo + ((ks_ * kTileBytes) >> 4);
+        const uint32_t ts = tb + C::tS + par * (NA * NR);
+        const uint32_t me = elect_one();
+        // the small parts first: the sum is truncated to its size at every step
+#pragma unroll
+        for (int a = NA - 1; a >= 0; --a)
+#pragma unroll
+          for (int p = NQ / NA - 1; p >= 0; --p)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ql = q_lo + (((a * (NQ / NA) + p) * NR * kD + k * 32) >> 4);
+              if (p < NQ / NA - 1 || k > 0)
+                umma_e4m3<true>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, idS);
+              else
+                umma_e4m3<false>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, idS);
+            }
+        umma_commit_if(me, &bS[par]);
+        umma_commit_if(me, &bKe[ks_]);
+        if (++ks_ == ST) {
+          ks_ = 0;
+          kph ^= 1;
+        }
       };
       issue_s(0, true);
 #pragma unroll 1
       for (int it = 0; it < n; ++it) {
+        const int par = it & 1;
         pos.next(d);
         const bool more = it + 1 < n, fresh = pos.lt == 0;
         // the next tile's scores run during this tile's softmax, unless they
         // wait for the next KV head's queries, which are staged after it
-        if (more && !fresh) issue_s(it + 1, false);
-        ok = ok && mbar_wait(&bP[it & 1], (it >> 1) & 1);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        const uint64_t dw = dw0 + static_cast<uint64_t>(((it & 1) * C::wbytes) >> 4);
-        const uint32_t to = tb + C::tO + (OB == 2 ? (it & 1) * NR : 0);
-        const uint32_t tv = tb + C::tV + (it & 1) * kVCols;
-        if (me) {
-#pragma unroll
-          for (int h = 1; h >= 0; --h)  // (the remainder first)
-#pragma unroll
-            for (int k = 0; k < kLineKeys / 16; ++k)
-              umma_f16_ta(to, tv + k * 8, dw + ((h * C::watoms * C::atom + k * 16 * 128) >> 4), idO,
-                          h == 0 || k > 0);
-          umma_commit(&bO[it & 1]);
-        }
+        if (more && !fresh) issue_s(par ^ 1, false);
+        mbar_wait_or(&bP[par], (it >> 1) & 1, s_fail);
         __syncwarp();
-        if (more && fresh) issue_s(it + 1, true);
+        tc_fence_after();
+        const uint32_t wl = w_lo + ((par * C::wbytes) >> 4);
+        const uint32_t to = tb + C::tO + par * NR, tv = tb + C::tV + par * kVCols;
+        const uint32_t me = elect_one();
+#pragma unroll
+        for (int h = 1; h >= 0; --h)  // (the remainder first)
+#pragma unroll
+          for (int k = 0; k < kLineKeys / 16; ++k) {
+            const uint32_t b = wl + ((h * C::atom + k * 16 * 128) >> 4);
+            if (h == 1 && k == 0)
+              umma_f16_ta<false>(me, to, tv + k * 8, b, w_hi, idR);
+            else
+              umma_f16_ta<true>(me, to, tv + k * 8, b, w_hi, h == 1 ? idR : idO);
+          }
+        umma_commit_if(me, &bO[par]);
+        if (more && fresh) issue_s(par ^ 1, true);
       }
-      if (!ok) *s_fail = 1;
-    } else if (warp == 14 && n > 0) {
+    } else if (warp == W0 + 6 && n > 0) {
       // ---- a tile's scales: lane p < 8 its page p's, read a tile ahead
       float k_ = 1.f, v_ = 1.f;
       auto fetch = [&]() {
@@ -357,26 +357,21 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       };
       fetch();
 #pragma unroll 1
-      for (int it = 0; it < n && ok; ++it) {
+      for (int it = 0; it < n; ++it) {
         const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
         const float v = fmaxf(v_, kMinScale);
-        const float4 w = make_float4(k_ * d.scale_log2, log2f(v), 1.f / v, 0.f);
         pos.next(d);
-        const int last = it + 1 == n || pos.lt == 0;
+        const bool last = it + 1 == n || pos.lt == 0;
+        const float4 w = make_float4(k_ * d.scale_log2, log2f(v), 1.f / v,
+                                     __int_as_float(nv + (last ? 256 : 0)));
         if (it + 1 < n) fetch();
         // (the info of two tiles back has been read)
-        if (it >= 2) ok = mbar_wait(&bP[it & 1], ((it - 2) >> 1) & 1);
-        TileInfo& t = info[it & 1];
-        if (lane < kLineKeys / kPS) t.page[lane] = w;
-        if (lane == 0) {
-          t.nv = nv;
-          t.last = last;
-        }
+        if (it >= 2) mbar_wait_or(&bP[it & 1], ((it - 2) >> 1) & 1, s_fail);
+        if (lane < kLineKeys / kPS) info[it & 1].page[lane] = w;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bS[it & 1]);
       }
-      if (!ok) *s_fail = 1;
-    } else if (warp < 12) {
+    } else if (warp < W0 + 4) {
       // ---- V codes -> fp16, transposed, into TMEM: warp w4 has the channels
       // 32 w4 .. (its TMEM lanes)
       const int w4 = warp & 3;
@@ -384,97 +379,92 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
 #pragma unroll 1
       for (int it = 0; it < n; ++it) {
         const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
-        ok = ok && mbar_wait(&bVf[it % ST], (it / ST) & 1);
+        mbar_wait_or(&bVf[it % ST], (it / ST) & 1, s_fail);
         const uint32_t vt = su32(vring + (it % ST) * kTileBytes);
-        uint32_t c[2][16];
+        // V^T of this parity is free once O = V W of two tiles back is done
+        if (it >= 2) mbar_wait_or(&bO[it & 1], ((it - 2) >> 1) & 1, s_fail);
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll
-        for (int dh = 0; dh < 2; ++dh)
+        for (int dh = 0; dh < 2; ++dh) {
+          uint32_t c[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = i * 16 + (lane & 15);
-            ldsm_b8_trans(vt + j * 128 + (((2 * w4 + dh) ^ (j & 7)) << 4), c[dh][2 * i],
-                          c[dh][2 * i + 1]);
+            ldsm_b8_trans(vt + j * 128 + (((2 * w4 + dh) ^ (j & 7)) << 4), c[2 * i], c[2 * i + 1]);
           }
-        if (nv < kLineKeys) {
-          // keys past the prefix may hold anything, and 0 times NaN is NaN
+          if (nv < kLineKeys) {
+            // keys past the prefix may hold anything, and 0 times NaN is NaN
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int m = min(max(nv - (i * 16 + 4 * (lane & 3)), 0), 4);
-            const uint32_t mask = m == 4 ? 0xffffffffu : (1u << (8 * m)) - 1u;
-#pragma unroll
-            for (int dh = 0; dh < 2; ++dh) {
-              c[dh][2 * i] &= mask;
-              c[dh][2 * i + 1] &= mask;
+            for (int i = 0; i < 8; ++i) {
+              const int m = min(max(nv - (i * 16 + 4 * (lane & 3)), 0), 4);
+              const uint32_t mask = m == 4 ? 0xffffffffu : (1u << (8 * m)) - 1u;
+              c[2 * i] &= mask;
+              c[2 * i + 1] &= mask;
             }
           }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bVe[it % ST]);
-        // V^T of this parity is free once O = V W of two tiles back is done
-        if (it >= 2) ok = ok && mbar_wait(&bO[it & 1], ((it - 2) >> 1) & 1);
-        tc_fence_after();
-#pragma unroll
-        for (int dh = 0; dh < 2; ++dh)
 #pragma unroll
           for (int kq = 0; kq < 2; ++kq) {
             uint32_t f[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              e4m3x4_to_f16x2(c[dh][kq * 8 + i], f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) e4m3x4_to_f16x2(c[kq * 8 + i], f[2 * i], f[2 * i + 1]);
             tmem_st16x256_x4_raw(tb + C::tV + (it & 1) * kVCols + kq * 32 + lane_off +
                                      (static_cast<uint32_t>(dh * 16) << 16),
                                  f);
           }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bVe[it % ST]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bP[it & 1]);
         pos.next(d);
       }
-      if (!ok) *s_fail = 1;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::soft_regs));
     // ---- softmax warps: warp w has TMEM lanes 32 (w % 4) .., keys of the S^T
-    // tile and channels of O^T; warp group w / 4 has the query columns
-    // [ch wg, ch wg + ch)
-    const int w4 = warp & 3, wg = warp >> 2, c0 = wg * C::ch;
+    // tile and channels of O^T; warp group w / 4 has the query columns c0 ..
+    const int w4 = warp & 3, wg = warp >> 2, c0 = wg * CW;
     const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
     const int key = 32 * w4 + lane;
-    u64 l[C::ch / 2], o[C::ch / 2];
-    int since = 0;  // tile of this KV head within the CTA
+    float* xg = xch + wg * 4 * CW;
+    float* ag = alpha + wg * CW;
+    u64 l[CW / 2], o[CW / 2];
     bool fresh = true;
-    uint32_t pend = 0;  // bit cc: chunk cc's O of the tile before has not been read yet
+    bool pend1 = false, pend2 = false;  // O of one / two tiles back is still to be read
 
-    // o += the columns of O buffer b (one MMA's result: a whole tile)
-    auto take_o = [&](int cc, int b) {
+    // o += O buffer b (one tile's product)
+    auto o_addr = [&](int b) { return tb + C::tO + b * NR + c0 + lane_off; };
+    auto add_o = [&](const float (&t)[CW]) {
 #pragma unroll
-      for (int i0 = 0; i0 < CW; i0 += (CW < 16 ? CW : 16)) {
-        float t[CW < 16 ? CW : 16];
-        tmem_ld(tb + C::tO + (OB == 2 ? b * NR : 0) + c0 + cc * CW + i0 + lane_off, t);
-#pragma unroll
-        for (int i = 0; i < (CW < 16 ? CW : 16); i += 2) {
-          u64& x = o[(cc * CW + i0 + i) / 2];
-          x = add2(x, pk(t[i], t[i + 1]));
-        }
-      }
+      for (int i = 0; i < CW; i += 2) o[i / 2] = add2(o[i / 2], pk(t[i], t[i + 1]));
     };
-    // the scores of chunk cc, as 2^x and columns: S rf kf + lv
-    auto load_x = [&](int it, int cc, u64 kf2, u64 lv2, u64 (&y)[CW / 2]) {
-      const int cb = c0 + cc * CW;
-      float a[CW];
-      tmem_ld(tb + C::tS + (it & 1) * (NA * NR) + cb + lane_off, a);
+    auto take_o = [&](int b) {
+      float t[CW];
+      tmem_ld_async(o_addr(b), t);
+      tmem_ld_wait(t);
+      add_o(t);
+    };
+    // the scores as exponents of 2, without the reference: S rf kf + lv
+    auto s_addr = [&](int it, int a) {
+      return tb + C::tS + (it & 1) * (NA * NR) + a * NR + c0 + lane_off;
+    };
+    auto to_x = [&](int it, u64 kf2, u64 lv2, const float (&a)[CW], u64 (&y)[CW / 2]) {
 #pragma unroll
       for (int i = 0; i < CW; i += 2) y[i / 2] = pk(a[i], a[i + 1]);
       if (NA == 2) {
-        tmem_ld(tb + C::tS + (it & 1) * (NA * NR) + NR + cb + lane_off, a);
+        float b[CW];
+        tmem_ld_async(s_addr(it, 1), b);
+        tmem_ld_wait(b);
         const u64 ps = pk(1.f / kPartScale, 1.f / kPartScale);
 #pragma unroll
-        for (int i = 0; i < CW; i += 2) y[i / 2] = fma2(pk(a[i], a[i + 1]), ps, y[i / 2]);
+        for (int i = 0; i < CW; i += 2) y[i / 2] = fma2(pk(b[i], b[i + 1]), ps, y[i / 2]);
       }
 #pragma unroll
       for (int i = 0; i < CW; i += 4) {
-        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(rf + cb + i);
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(rf + c0 + i);
         y[i / 2] = fma2(mul2(y[i / 2], r.x), kf2, lv2);
         y[i / 2 + 1] = fma2(mul2(y[i / 2 + 1], r.y), kf2, lv2);
       }
@@ -484,16 +474,24 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
       if (fresh) {
         // ---- a KV head begins: its queries, in parts (the S MMAs that read
         // the previous head's are done: this thread has waited for them)
-        since = 0;
-        pend = 0;
+        pend1 = pend2 = false;
 #pragma unroll
-        for (int i = 0; i < C::ch / 2; ++i) l[i] = o[i] = 0ull;
-        bar_sync(3, kSoftmaxThreads);
+        for (int i = 0; i < CW / 2; ++i) l[i] = o[i] = 0ull;
         const size_t q0 = ((static_cast<size_t>(pos.s) * d.Hq + pos.g * d.G) * d.B + r0) * kD;
-#pragma unroll 1
-        for (int r = warp; r < NR; r += 8) {
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < nrows) x = ld4(Q, q0 + static_cast<size_t>(r) * kD + 4 * lane, d.dtype);
+        // (all of the warp's rows in flight at once)
+        float4 xr[NR / W0];
+#pragma unroll
+        for (int i = 0; i < NR / W0; ++i) {
+          const int r = warp + i * W0;
+          xr[i] = r < nrows ? ld4(Q, q0 + static_cast<size_t>(r) * kD + 4 * lane,
+                                  NQ == 2 ? LOSA_BF16 : LOSA_F32)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        bar_sync(5, NS);
+#pragma unroll
+        for (int i = 0; i < NR / W0; ++i) {
+          const int r = warp + i * W0;
+          float4 x = xr[i];
           const float amax = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
           const int c = 7 - max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -119);
           const float sc = exp2_int(c);
@@ -514,190 +512,170 @@ __global__ void __launch_bounds__(kThreadsQ, 1)
           }
         }
         fence_async_smem();
-        bar_sync(3, kSoftmaxThreads);
+        bar_sync(5, NS);
         if (lane == 0) mbar_arrive(bQ);
       }
       // S^T of this tile and all MMAs issued before it are done: O = V W of two
-      // tiles back too, so W's buffer of this parity is free
-      ok = ok && mbar_wait(&bS[it & 1], (it >> 1) & 1);
+      // tiles back too, so that may be read and W's buffer of this parity is free
+      mbar_wait_or(&bS[it & 1], (it >> 1) & 1, s_fail);
+      __syncwarp();
       tc_fence_after();
-      const TileInfo& ti = info[it & 1];
-      const int nv = ti.nv;
-      const bool last = ti.last;
-      const float4 pg = ti.page[key >> 4];
+      float sc[CW];
+      tmem_ld_async(s_addr(it, 0), sc);
+      const float4 pg = info[it & 1].page[key >> 4];
+      const int nv = __float_as_int(pg.w) & 255;
+      const bool last = __float_as_int(pg.w) >= 256;
       const bool valid = key < nv;
       const u64 kf2 = pk(pg.x, pg.x), lv2 = pk(pg.y, pg.y);
       const float rv = valid ? pg.z : 0.f;
       const u64 rv2 = pk(rv, rv);
-      char* wb = wbuf + (it & 1) * C::wbytes;
+      if (pend2) take_o(it & 1);
+      tmem_ld_wait(sc);
+      u64 y[CW / 2];
+      to_x(it, kf2, lv2, sc, y);
+      float top = -INFINITY;
 #pragma unroll
-      for (int cc = 0; cc < NCH; ++cc) {
-        const int cb = c0 + cc * CW;  // first column
-        u64 y[CW / 2];
-        load_x(it, cc, kf2, lv2, y);
-        float top = -INFINITY;
+      for (int i = 0; i < CW; i += 4) {
+        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + c0 + i);
+        y[i / 2] = add2(y[i / 2], m.x);
+        y[i / 2 + 1] = add2(y[i / 2 + 1], m.y);
+        const float2 a = up(y[i / 2]), b = up(y[i / 2 + 1]);
+        top = max3(max3(top, a.x, a.y), b.x, b.y);
+      }
+      pend2 = pend1;
+      if (bar_or(1 + wg, 128, valid && top > kRefMove)) {
+        // ---- some row's reference moves (the first tile; then seldom): the
+        // columns' maxima over the tile's keys, references, and what has been
+        // accumulated against the old ones
+        tmem_ld_async(s_addr(it, 0), sc);
+        tmem_ld_wait(sc);
+        to_x(it, kf2, lv2, sc, y);
+        float mine = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < CW; i += 4) {
-          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + cb + i);
-          y[i / 2] = add2(y[i / 2], m.x);
-          y[i / 2 + 1] = add2(y[i / 2 + 1], m.y);
-          const float2 a = up(y[i / 2]), b = up(y[i / 2 + 1]);
-          top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
+        for (int i = 0; i < CW; i += 2) {
+          const float2 a = up(y[i / 2]);
+          const float m0 = redux_max(valid ? a.x : -INFINITY);
+          const float m1 = redux_max(valid ? a.y : -INFINITY);
+          if (lane == i) mine = m0;
+          if (lane == i + 1) mine = m1;
         }
-        if (OB == 2 && since >= 2) {
-          // O of two tiles back (unless a moved reference has taken it already)
-          if (pend & (2u << (2 * cc))) take_o(cc, it & 1);
+        if (lane < CW) xg[w4 * CW + lane] = mine;
+        bar_sync(1 + wg, 128);
+        if (w4 == 0 && lane < CW) {
+          float m = mine;
+#pragma unroll
+          for (int w = 1; w < 4; ++w) m = fmaxf(m, xg[w * CW + lane]);
+          const float old = -nm[c0 + lane];
+          const bool move = m > old + kRefMove || (old == -INFINITY && m > old);
+          const float ref = move ? m - kRefTop : old;
+          ag[lane] = move ? exp2f(old - ref) : 1.f;
+          nm[c0 + lane] = -ref;
         }
-        pend = (pend & ~(2u << (2 * cc))) | ((pend & (1u << (2 * cc))) << 1);
-        if (bar_or(1 + wg, 128, valid && top > kRefMove)) {
-          // ---- some row's reference moves (the first tile; then seldom): the
-          // columns' maxima over the tile's keys, references, and what has been
-          // accumulated against the old ones
-          load_x(it, cc, kf2, lv2, y);
-          float mine = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < CW; i += 2) {
-            const float2 a = up(y[i / 2]);
-            const float m0 = redux_max(valid ? a.x : -INFINITY);
-            const float m1 = redux_max(valid ? a.y : -INFINITY);
-            if (lane == i) mine = m0;
-            if (lane == i + 1) mine = m1;
-          }
-          if (lane < CW) xch[(wg * 4 + w4) * 32 + lane] = mine;
-          bar_sync(1 + wg, 128);
-          if (w4 == 0 && lane < CW) {
-            float m = mine;
-#pragma unroll
-            for (int w = 1; w < 4; ++w) m = fmaxf(m, xch[(wg * 4 + w) * 32 + lane]);
-            const float old = -nm[cb + lane];
-            const bool move = m > old + kRefMove || (old == -INFINITY && m > old);
-            const float ref = move ? m - kRefTop : old;
-            alpha[wg * 32 + lane] = move ? exp2f(old - ref) : 1.f;
-            nm[cb + lane] = -ref;
-          }
-          bar_sync(1 + wg, 128);
-          if (since > 0) {
-            if (pend & (2u << (2 * cc))) {  // the tile before's
-              ok = ok && mbar_wait(&bO[(it - 1) & 1], ((it - 1) >> 1) & 1);
-              tc_fence_after();
-              take_o(cc, (it - 1) & 1);
-              pend &= ~(2u << (2 * cc));
-            }
-#pragma unroll
-            for (int i = 0; i < CW; i += 2) {
-              const u64 a = *reinterpret_cast<const u64*>(alpha + wg * 32 + i);
-              o[(cc * CW + i) / 2] = mul2(o[(cc * CW + i) / 2], a);
-              l[(cc * CW + i) / 2] = mul2(l[(cc * CW + i) / 2], a);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < CW; i += 2)
-            y[i / 2] = add2(y[i / 2], *reinterpret_cast<const u64*>(nm + cb + i));
-          // (the next vote's slow path writes xch, nm and alpha only after a
-          // barrier of this warp group)
-        }
-        if (nv < kLineKeys) {
-          const u64 none = pk(-INFINITY, -INFINITY);
-#pragma unroll
-          for (int i = 0; i < CW / 2; ++i) y[i] = valid ? y[i] : none;
-        }
-#pragma unroll
-        for (int i = 0; i < CW; i += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 a = up(y[i / 2 + u]);
-            const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            const u64 w2 = pk(w.x, w.y);
-            u64& lx = l[(cc * CW + i) / 2 + u];
-            lx = fma2(w2, rv2, lx);
-            hi[u] = pack_f16x2(w.x, w.y);
-            const float2 f = f16x2_to_f32(hi[u]);
-            const float2 r = up(fma2(pk(f.x, f.y), pk(-1.f, -1.f), w2));
-            lo[u] = pack_f16x2(r.x, r.y);
-          }
-          const int col = cb + i;  // its 16-byte chunk of the key's row
-          char* dst = wb + (col >> 6) * C::atom + key * 128 + ((((col & 63) >> 3) ^ (key & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + C::watoms * C::atom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        if (OB == 1 && since > 0 && (pend & (2u << (2 * cc)))) {
-          // one O buffer: the tile before's result, before this tile's MMA
-          if (cc == 0) ok = ok && mbar_wait(&bO[(it - 1) & 1], ((it - 1) >> 1) & 1);
+        bar_sync(1 + wg, 128);
+        if (pend2) {  // the tile before's product, against the old references too
+          mbar_wait_or(&bO[(it - 1) & 1], ((it - 1) >> 1) & 1, s_fail);
+          __syncwarp();
           tc_fence_after();
-          take_o(cc, 0);
-          pend &= ~(2u << (2 * cc));
+          take_o((it - 1) & 1);
+          pend2 = false;
         }
-        pend |= 1u << (2 * cc);
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) {
+          const u64 a = *reinterpret_cast<const u64*>(ag + i);
+          o[i / 2] = mul2(o[i / 2], a);
+          l[i / 2] = mul2(l[i / 2], a);
+          y[i / 2] = add2(y[i / 2], *reinterpret_cast<const u64*>(nm + c0 + i));
+        }
+        // (the next vote's slow path writes xch, nm and alpha only after a
+        // barrier of this warp group)
+      }
+      pend1 = true;
+      if (nv < kLineKeys) {
+        const u64 none = pk(-INFINITY, -INFINITY);
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i) y[i] = valid ? y[i] : none;
+      }
+      char* wrow = wbuf + (it & 1) * C::wbytes + key * 128;
+#pragma unroll
+      for (int i = 0; i < CW; i += 8) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 a = up(y[i / 2 + u]);
+          const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+          const u64 w2 = pk(w.x, w.y);
+          l[i / 2 + u] = fma2(w2, rv2, l[i / 2 + u]);
+          hi[u] = pack_f16x2(w.x, w.y);
+          const float2 r = f16x2_sub(hi[u], w);  // minus the remainder
+          lo[u] = pack_f16x2(r.x, r.y);
+        }
+        // the 16-byte chunk of these columns in the key's row
+        char* dst = wrow + ((((c0 + i) >> 3) ^ (key & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + C::atom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bP[it & 1]);
-      ++since;
       fresh = last;
 
       if (last) {
         // ---- the KV head ends here: the partial of its rows
-        ok = ok && mbar_wait(&bO[it & 1], (it >> 1) & 1);  // (in order: the tile before's too)
+        mbar_wait_or(&bO[it & 1], (it >> 1) & 1, s_fail);  // (in order: the tile before's too)
+        __syncwarp();
         tc_fence_after();
-        if (!__all_sync(0xffffffffu, ok) && lane == 0) *s_fail = 1;
         const int sg = pos.s * d.Hkv + pos.g;
         float* dst0 = part + ((static_cast<size_t>(blockIdx.x) + sg) * rows + r0) * kPartStride;
+        if (pend2) take_o((it - 1) & 1);
+        take_o(it & 1);
+        // sums over the lanes: after the exchange of halves, lane i / (32 / CW)
+        // holds column i's
+        float v[CW];
 #pragma unroll
-        for (int cc = 0; cc < NCH; ++cc) {
-          const int cb = c0 + cc * CW;
-          if (OB == 2 && (pend & (2u << (2 * cc)))) take_o(cc, (it - 1) & 1);
-          take_o(cc, it & 1);
-          // sums over the lanes: after the exchange of halves, lane i / (32 / CW)
-          // holds column i's
-          float v[CW];
+        for (int i = 0; i < CW; i += 2) {
+          const float2 a = up(l[i / 2]);
+          v[i] = a.x;
+          v[i + 1] = a.y;
+        }
+        int w = CW;
 #pragma unroll
-          for (int i = 0; i < CW; i += 2) {
-            const float2 a = up(l[(cc * CW + i) / 2]);
-            v[i] = a.x;
-            v[i + 1] = a.y;
-          }
-          int w = CW;
+        for (int sh = 16; sh > 0; sh >>= 1) {
+          if (w > 1) {
+            w >>= 1;
+            const bool hi = lane & sh;
 #pragma unroll
-          for (int sh = 16; sh > 0; sh >>= 1) {
-            if (w > 1) {
-              w >>= 1;
-              const bool hi = lane & sh;
-#pragma unroll
-              for (int i = 0; i < CW / 2; ++i) {
-                if (i < w) {
-                  const float send = hi ? v[i] : v[i + w], keep = hi ? v[i + w] : v[i];
-                  v[i] = keep + __shfl_xor_sync(0xffffffffu, send, sh);
-                }
+            for (int i = 0; i < CW / 2; ++i) {
+              if (i < w) {
+                const float send = hi ? v[i] : v[i + w], keep = hi ? v[i + w] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, sh);
               }
-            } else {
-              v[0] += __shfl_xor_sync(0xffffffffu, v[0], sh);
             }
+          } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], sh);
           }
-          bar_sync(1 + wg, 128);  // (xch: the maxima, or the chunk before, have been read)
-          if (lane % (32 / CW) == 0) xch[(wg * 4 + w4) * 32 + lane / (32 / CW)] = v[0];
-          bar_sync(1 + wg, 128);
-          const bool good = *s_fail == 0;
+        }
+        bar_sync(1 + wg, 128);  // (xch: the maxima have been read)
+        if (lane % (32 / CW) == 0) xg[w4 * CW + lane / (32 / CW)] = v[0];
+        bar_sync(1 + wg, 128);
+        const bool good = *s_fail == 0;
 #pragma unroll
-          for (int i = 0; i < CW; i += 2) {
-            const float2 a = up(o[(cc * CW + i) / 2]);
-            if (good && cb + i < nrows) dst0[(cb + i) * kPartStride + 4 + key] = a.x;
-            if (good && cb + i + 1 < nrows) dst0[(cb + i + 1) * kPartStride + 4 + key] = a.y;
-          }
-          if (good && w4 == 0 && lane < CW && cb + lane < nrows) {
-            float sum = 0.f;
+        for (int i = 0; i < CW; i += 2) {
+          const float2 a = up(o[i / 2]);
+          if (good && c0 + i < nrows) dst0[(c0 + i) * kPartStride + 4 + key] = a.x;
+          if (good && c0 + i + 1 < nrows) dst0[(c0 + i + 1) * kPartStride + 4 + key] = a.y;
+        }
+        if (good && w4 == 0 && lane < CW && c0 + lane < nrows) {
+          float sum = 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sum += xch[(wg * 4 + q) * 32 + lane];
-            float* dst = dst0 + (cb + lane) * kPartStride;
-            dst[0] = -nm[cb + lane];
-            dst[1] = sum;
-          }
+          for (int q = 0; q < 4; ++q) sum += xg[q * CW + lane];
+          float* dst = dst0 + (c0 + lane) * kPartStride;
+          dst[0] = -nm[c0 + lane];
+          dst[1] = sum;
         }
         pos.next_head(d);
       }
     }
-    if (!__all_sync(0xffffffffu, ok) && lane == 0) *s_fail = 1;
   }
   tc_fence_before();
   __syncthreads();
@@ -725,7 +703,7 @@ int launch_partials(const Dims& d, const void* q, const void* k8, const void* v8
   if (make_byte_tmap(&kmap, k8, nrows, kLineKeys) != LOSA_OK ||
       make_byte_tmap(&vmap, v8, nrows, kLineKeys) != LOSA_OK)
     return record_cuda_error(cudaErrorInvalidValue);
-  fn<<<dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR), kThreadsQ, C::smem, st>>>(
+  fn<<<dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR), C::threads, C::smem, st>>>(
       q, kmap, vmap, k_scale, v_scale, part, status, d);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
@@ -766,8 +744,7 @@ extern "C" int losa_dense_prefix_quant(const losa_shape* shape, const void* q, c
   const int r = d.G * d.B;
   auto* launch = d.dtype == LOSA_BF16 ? (r <= 16   ? launch_partials<16, 2>
                                          : r <= 32 ? launch_partials<32, 2>
-                                         : r <= 64 ? launch_partials<64, 2>
-                                                   : launch_partials<128, 2>)
+                                                   : launch_partials<64, 2>)
                                       : (r <= 16 ? launch_partials<16, 6> : launch_partials<64, 6>);
   rc = launch(d, q, k8, v8, k_scale, v_scale, part, status, st);
   if (rc != LOSA_OK) return rc;

@@ -301,11 +301,8 @@ inline bool any_write_alias(const Region* r, int n) {
 }
 
 int make_dims(const losa_shape* sh, int which, Dims* d);
-// Row halves of the dense pass over an 8-bit prefix: fp32 queries take six
-// e4m3 parts each, and 128 rows of them do not fit beside the rest.
-inline int dense_quant_halves(const Dims& d) {
-  return d.dtype == LOSA_F32 && d.G * d.B > 64 ? 2 : 1;
-}
+// CTAs that share the keys of a range of the line: 64 query rows each.
+inline int dense_quant_halves(const Dims& d) { return d.G * d.B > 64 ? 2 : 1; }
 // Whether the fused step kernel's shared-memory plan fits in `max_dyn` bytes.
 bool fused_step_fits(const Dims& d, int max_dyn);
 // Dynamic shared memory a B200 CTA may opt in to (227 KB).

@@ -85,6 +85,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     if (clock64() - t0 > kWaitCycles) return false;
   return true;
 }
+// Bounded wait for phase `parity` of `bar`, for a block whose threads share
+// the flag `fail` (shared memory): a wait that gives up sets it, and ends the
+// waits of the others.  What follows a failed wait works on whatever is there
+// (all of it in bounds); its results are not used.
+__device__ __forceinline__ void mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  const long long t0 = clock64();
+  while (!mbar_try_sleep(bar, parity, 20000u)) {
+    if (*fail) return;
+    if (clock64() - t0 > kWaitCycles) {
+      *fail = 1;
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_wait_or(uint64_t* bar, uint32_t parity, int* fail) {
+  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, fail);
+}
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
                                         uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -128,6 +145,10 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
+// An arrival at named barrier `id` of `n` threads, without waiting.
+__device__ __forceinline__ void bar_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 // The same barrier, and whether `p` held for any of its threads.
 __device__ __forceinline__ bool bar_or(int id, int n, bool p) {
   uint32_t r;
@@ -152,6 +173,20 @@ __device__ __forceinline__ void ldsm_b8_trans(uint32_t addr, uint32_t& r0, uint3
   asm volatile("ldmatrix.sync.aligned.m16n16.x1.trans.shared.b8 {%0,%1}, [%2];"
                : "=r"(r0), "=r"(r1)
                : "r"(addr));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (the fp16 numbers of h) - x, exact where the difference is an fp32 number.
+__device__ __forceinline__ float2 f16x2_sub(uint32_t h, float2 x) {
+  float2 r;
+  asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n sub.f32.f16 %0, l, %3;\n"
+      " sub.f32.f16 %1, h, %4;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(h), "f"(x.x), "f"(x.y));
+  return r;
 }
 // Two fp32 values -> packed fp16x2 (round to nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
