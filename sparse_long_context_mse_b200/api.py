@@ -9,6 +9,7 @@ call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -365,48 +366,103 @@ def alloc_quant_prefix(sh: Shape, device):
             torch.ones(sc, dtype=torch.float32, device=device))
 
 
-def _quant_ptrs(sh: Shape, k8, v8, k_scale, v_scale, dev):
-    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
-    sc = (sh.num_seqs, sh.n_kv_heads, sh.capacity_pages)
-    return [_ptr(k8, kv, torch.float8_e4m3fn, "k8", dev),
-            _ptr(v8, kv, torch.float8_e4m3fn, "v8", dev),
-            _ptr(k_scale, sc, torch.float32, "k_scale", dev),
-            _ptr(v_scale, sc, torch.float32, "v_scale", dev)]
+# The 8-bit calls have a workspace of their own kind and up to 17 tensors each; their
+# checks run in native code (csrc/torch_binding.cpp), which also makes the tensors'
+# device current and takes its current stream.  One character per tensor says what
+# it has to be; a small letter other than s and b marks an optional one.
+_binding = None
+
+
+def _native():
+    """The native checks (raises if they were not built)."""
+    global _binding
+    if _binding is None:
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m sparse_long_context_mse_b200.build`")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.use(_address("losa_page_meta_size"))
+        _binding = m
+    return _binding
+
+
+_addresses = {}
+
+
+def _address(name: str) -> int:
+    """Address of an entry point of the loaded library."""
+    a = _addresses.get(name)
+    if a is None:
+        a = _addresses[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    return a
+
+
+def _expected(sh: Shape, kind: str):
+    """``(shape, dtype)`` of a tensor of that kind (shape None: any)."""
+    S, Hq, Hkv, B, d = sh.num_seqs, sh.n_q_heads, sh.n_kv_heads, sh.block_size, sh.head_dim
+    return {
+        "Q": ((S, Hq, B, d), sh.torch_dtype), "K": ((S, Hkv, sh.capacity, d), sh.torch_dtype),
+        "8": ((S, Hkv, sh.capacity, d), torch.float8_e4m3fn),
+        "s": ((S, Hkv, sh.capacity_pages), torch.float32),
+        "b": ((S, Hkv, B, d), sh.torch_dtype), "o": ((S, Hq, B, d), torch.float32),
+        "l": ((S, Hq, B), torch.float32), "a": ((S, Hq, sh.n_active), torch.int32),
+        "p": ((S, Hq, sh.n_active, sh.pages_per_row), torch.int32), "u": ((S, Hkv), torch.int32),
+        "m": ((page_meta_size(sh),), torch.uint8), "W": (None, torch.uint8),
+    }[kind if kind in "QK8sbW" else kind.lower()]
+
+
+def _refuse(sh: Shape, kinds: str, names, tensors):
+    """Raise for the first tensor that is not what its kind says."""
+    dev = None
+    for kind, name, t in zip(kinds, names, tensors):
+        if t is None and kind in "olapum":
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        dev = _device_of(t) if dev is None else dev
+        _ptr(t, *_expected(sh, kind), name, dev)
+    raise ValueError("the call's tensors are not what its shape says")
+
+
+def _invoke(entry: str, sh: Shape, kinds: str, names, tensors, stream):
+    lens = getattr(sh, "_prefix_lens", None)
+    if lens is not None and sh.prefix_lens:
+        _call_device(sh, tensors[0])
+    rc = _native().call(_address(entry), sh, kinds, tensors,
+                        None if stream is None else stream.cuda_stream)
+    if rc == -1:
+        _refuse(sh, kinds, names, tensors)
+    _check(rc)
+
+
+_CACHE = ("k8", "v8", "k_scale", "v_scale")
 
 
 def quantize_prefix(sh: Shape, k_prefix, v_prefix, k8, v8, k_scale, v_scale, page_meta=None,
                     stream=None):
     """``losa_quantize_prefix``: the prefix as e4m3 codes and page scales, and
     (unless ``page_meta`` is None) the page metadata of the keys they stand for."""
-    dev = _call_device(sh, k_prefix)
-    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
-    args = [_ptr(k_prefix, kv, sh.torch_dtype, "k_prefix", dev),
-            _ptr(v_prefix, kv, sh.torch_dtype, "v_prefix", dev),
-            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
-            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev)]
-    _check(lib().losa_quantize_prefix(ctypes.byref(sh), *args, _stream(stream)))
+    _invoke("losa_quantize_prefix", sh, "KK88ssm", ("k_prefix", "v_prefix", *_CACHE, "page_meta"),
+            (k_prefix, v_prefix, k8, v8, k_scale, v_scale, page_meta), stream)
 
 
 def append_block_quant(sh: Shape, k_blk, v_blk, k8, v8, k_scale, v_scale, page_meta=None,
                        stream=None):
     """``losa_append_block_quant``: :func:`append_block` for an 8-bit prefix."""
-    dev = _call_device(sh, k_blk)
-    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
-    args = [_ptr(k_blk, kb, sh.torch_dtype, "k_blk", dev),
-            _ptr(v_blk, kb, sh.torch_dtype, "v_blk", dev),
-            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
-            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev)]
-    _check(lib().losa_append_block_quant(ctypes.byref(sh), *args, _stream(stream)))
+    _invoke("losa_append_block_quant", sh, "bb88ssm", ("k_blk", "v_blk", *_CACHE, "page_meta"),
+            (k_blk, v_blk, k8, v8, k_scale, v_scale, page_meta), stream)
 
 
 def dequantize_prefix(sh: Shape, k8, v8, k_scale, v_scale, k_prefix, v_prefix, stream=None):
     """``losa_dequantize_prefix``: read an 8-bit prefix back in the shape's dtype."""
-    dev = _call_device(sh, k8)
-    kv = (sh.num_seqs, sh.n_kv_heads, sh.capacity, sh.head_dim)
-    args = [*_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
-            _ptr(k_prefix, kv, sh.torch_dtype, "k_prefix", dev),
-            _ptr(v_prefix, kv, sh.torch_dtype, "v_prefix", dev)]
-    _check(lib().losa_dequantize_prefix(ctypes.byref(sh), *args, _stream(stream)))
+    _invoke("losa_dequantize_prefix", sh, "88ssKK", (*_CACHE, "k_prefix", "v_prefix"),
+            (k8, v8, k_scale, v_scale, k_prefix, v_prefix), stream)
+
+
+_DENSE_NAMES = ("q", *_CACHE, "k_blk", "v_blk", "o_p", "l_p", "out", "out_lse", "workspace")
 
 
 def dense_prefix_quant(sh: Shape, q, k8, v8, k_scale, v_scale, k_blk, v_blk, o_p, l_p, out,
@@ -414,60 +470,30 @@ def dense_prefix_quant(sh: Shape, q, k8, v8, k_scale, v_scale, k_blk, v_blk, o_p
     """``losa_dense_prefix_quant``: :func:`dense_prefix` over an 8-bit prefix
     (``block_size`` 1: the attention of one decoded token).  The workspace is of
     kind ``LOSA_WS_DENSE_QUANT``."""
-    dev = _call_device(sh, q)
-    dt = sh.torch_dtype
-    qs = (sh.num_seqs, sh.n_q_heads, sh.block_size, sh.head_dim)
-    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
-    rs = qs[:3]
-    args = [_ptr(q, qs, dt, "q", dev), *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
-            _ptr(k_blk, kb, dt, "k_blk", dev), _ptr(v_blk, kb, dt, "v_blk", dev),
-            _ptr(o_p, qs, torch.float32, "o_p", dev), _ptr(l_p, rs, torch.float32, "l_p", dev),
-            _ptr(out, qs, torch.float32, "out", dev),
-            _ptr(out_lse, rs, torch.float32, "out_lse", dev),
-            _ptr(workspace, None, torch.uint8, "workspace", dev)]
-    _check(lib().losa_dense_prefix_quant(ctypes.byref(sh), *args, workspace.numel(),
-                                         _stream(stream)))
+    _invoke("losa_dense_prefix_quant", sh, "Q88ssbbOLOlW", _DENSE_NAMES,
+            (q, k8, v8, k_scale, v_scale, k_blk, v_blk, o_p, l_p, out, out_lse, workspace), stream)
+
+
+_STEP_NAMES = ("q_cur", "q_prev", *_CACHE, "page_meta", "k_blk", "v_blk", "o_p", "l_p", "out",
+               "out_lse", "active_idx", "page_idx", "union_count", "workspace")
 
 
 def step_quant(sh: Shape, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk, o_p,
                l_p, out, out_lse, workspace, active_idx=None, page_idx=None, union_count=None,
                stream=None):
     """``losa_step_quant``: :func:`step` over an 8-bit prefix."""
-    _step_quant_call("losa_step_quant", sh, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta,
-                     k_blk, v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx,
-                     union_count, stream)
+    _invoke("losa_step_quant", sh, "QQ88ssMbbOLOlapuW", _STEP_NAMES,
+            (q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk, o_p, l_p, out,
+             out_lse, active_idx, page_idx, union_count, workspace), stream)
 
 
 def step_ref_quant(sh: Shape, q_cur, q_ref, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk,
                    o_p, l_p, out, out_lse, workspace, active_idx=None, page_idx=None,
                    union_count=None, stream=None):
     """``losa_step_ref_quant``: :func:`step_ref` over an 8-bit prefix."""
-    _step_quant_call("losa_step_ref_quant", sh, q_cur, q_ref, k8, v8, k_scale, v_scale, page_meta,
-                     k_blk, v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx,
-                     union_count, stream)
-
-
-def _step_quant_call(fn, sh: Shape, q_cur, q_prev, k8, v8, k_scale, v_scale, page_meta, k_blk,
-                     v_blk, o_p, l_p, out, out_lse, workspace, active_idx, page_idx, union_count,
-                     stream):
-    dev = _call_device(sh, q_cur)
-    dt = sh.torch_dtype
-    qs = (sh.num_seqs, sh.n_q_heads, sh.block_size, sh.head_dim)
-    kb = (sh.num_seqs, sh.n_kv_heads, sh.block_size, sh.head_dim)
-    rs = qs[:3]
-    A, k = sh.n_active, sh.pages_per_row
-    args = [_ptr(q_cur, qs, dt, "q_cur", dev), _ptr(q_prev, qs, dt, "q_prev", dev),
-            *_quant_ptrs(sh, k8, v8, k_scale, v_scale, dev),
-            _ptr(page_meta, (page_meta_size(sh),), torch.uint8, "page_meta", dev),
-            _ptr(k_blk, kb, dt, "k_blk", dev), _ptr(v_blk, kb, dt, "v_blk", dev),
-            _ptr(o_p, qs, torch.float32, "o_p", dev), _ptr(l_p, rs, torch.float32, "l_p", dev),
-            _ptr(out, qs, torch.float32, "out", dev),
-            _ptr(out_lse, rs, torch.float32, "out_lse", dev),
-            _ptr(active_idx, (sh.num_seqs, sh.n_q_heads, A), torch.int32, "active_idx", dev),
-            _ptr(page_idx, (sh.num_seqs, sh.n_q_heads, A, k), torch.int32, "page_idx", dev),
-            _ptr(union_count, (sh.num_seqs, sh.n_kv_heads), torch.int32, "union_count", dev),
-            _ptr(workspace, None, torch.uint8, "workspace", dev)]
-    _check(getattr(lib(), fn)(ctypes.byref(sh), *args, workspace.numel(), _stream(stream)))
+    _invoke("losa_step_ref_quant", sh, "QQ88ssMbbOLOlapuW", _STEP_NAMES,
+            (q_cur, q_ref, k8, v8, k_scale, v_scale, page_meta, k_blk, v_blk, o_p, l_p, out,
+             out_lse, active_idx, page_idx, union_count, workspace), stream)
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:

@@ -1,4 +1,5 @@
-"""Build step of the CUDA library: ``csrc/*.cu`` -> ``liblosa.so`` (in-tree).
+"""Build step of the CUDA library: ``csrc/*.cu`` -> ``liblosa.so`` (in-tree), and
+of the binding's native argument checks: ``csrc/torch_binding.cpp`` -> ``_binding.so``.
 
 nvcc cross-compiles for sm_100a; no GPU is needed to build.
 ``python -m sparse_long_context_mse_b200.build`` rebuilds when a source or
@@ -18,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblosa.so")
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 OBJDIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -42,10 +45,41 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or _binding_stale():
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _binding_deps():
+    return [BINDING_SRC, os.path.join(INCLUDE, "losa.h"), os.path.abspath(__file__)]
+
+
+def _binding_stale() -> bool:
+    return not os.path.exists(BINDING) or any(
+        os.path.getmtime(p) > os.path.getmtime(BINDING) for p in _binding_deps())
+
+
+def build_binding(force: bool = False) -> str:
+    """The native argument checks, against the installed torch's headers."""
+    if not force and not _binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-isystem", inc, "-isystem", cuda,
+           "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda"]  # (loaded already: the package imports torch first)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 TRACE_LIB = os.path.join(PKG, "liblosa_trace.so")
@@ -56,6 +90,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
     """The library; with ``trace`` a separate copy, ``liblosa_trace.so``,
     whose step kernel records per-phase timestamps (``phase_trace.py``)."""
     lib = TRACE_LIB if trace else LIB
+    build_binding(force)
     if not force and os.path.exists(lib) and all(
             os.path.getmtime(p) <= os.path.getmtime(lib) for p in _deps()):
         return lib

@@ -140,19 +140,60 @@ def test_too_many_groups(L, no_device):
         assert invoke(L, name, sh, [(i + 1) << 42 for i in range(20)]) == UNS, name
 
 
-def test_binding_refuses_host_tensors_and_wrong_types():
+def test_binding_refuses_host_tensors_and_wrong_types(L, monkeypatch):
     sh = S(prefix_len=32)
     k = torch.zeros(1, 8, 32, 128, dtype=torch.bfloat16)
     c8 = torch.zeros(1, 8, 32, 128, dtype=torch.float8_e4m3fn)
     sc = torch.ones(1, 8, 2)
-    with pytest.raises(ValueError):  # a host tensor
-        api.quantize_prefix(sh, k, k, c8, c8, sc, sc)
-    cpu = torch.device("cpu")
-    assert len(api._quant_ptrs(sh, c8, c8, sc, sc, cpu)) == 4
-    for bad in ((k, c8, sc, sc), (c8[:, :, :31], c8, sc, sc), (c8, c8, sc[..., :1], sc),
-                (c8, c8, sc, sc.double()), (c8, c8.transpose(1, 2), sc, sc)):
-        with pytest.raises(ValueError):
-            api._quant_ptrs(sh, *bad, cpu)
+    for bad in ((k, k, c8, c8, sc, sc), (k, k, c8, c8, sc, sc, torch.zeros(3, dtype=torch.uint8))):
+        with pytest.raises(ValueError):  # host tensors
+            api.quantize_prefix(sh, *bad)
+    with pytest.raises(TypeError):
+        api.quantize_prefix(sh, [0.0], k, c8, c8, sc, sc)
+    monkeypatch.setattr(api, "_device_of", lambda t: t.device)
+    with pytest.raises(TypeError):  # only the metadata may be left out
+        api.quantize_prefix(sh, k, k, c8, None, sc, sc)
+
+
+@pytest.mark.parametrize("kind,good,bad", [
+    ("8", torch.zeros(1, 8, 32, 128, dtype=torch.float8_e4m3fn),
+     [torch.zeros(1, 8, 32, 128, dtype=torch.uint8), torch.zeros(1, 8, 31, 128, dtype=torch.float8_e4m3fn),
+      torch.zeros(1, 8, 32, 256, dtype=torch.float8_e4m3fn)[..., ::2]]),
+    ("s", torch.ones(1, 8, 2), [torch.ones(1, 8, 3), torch.ones(1, 8, 2).double(), torch.ones(8, 2)]),
+    ("b", torch.zeros(1, 8, 16, 128, dtype=torch.bfloat16),
+     [torch.zeros(1, 8, 16, 128), torch.zeros(1, 8, 16, 256, dtype=torch.bfloat16)[..., ::2]]),
+    ("m", None, [torch.zeros(5, dtype=torch.uint8)])])
+def test_binding_says_which_tensor_is_wrong(L, monkeypatch, kind, good, bad):
+    """The message names the tensor (host tensors stand in: only the device check is
+    taken out)."""
+    monkeypatch.setattr(api, "_device_of", lambda t: t.device)
+    sh = S(prefix_len=32)
+    first = torch.zeros(1, 32, 16, 128, dtype=torch.bfloat16)
+    for t in bad:
+        with pytest.raises(ValueError, match="the_one"):
+            api._refuse(sh, "Q" + kind, ("q", "the_one"), (first, t))
+    with pytest.raises(ValueError, match="not what its shape says"):  # nothing to name
+        api._refuse(sh, "Q" + kind, ("q", "the_one"), (first, good))
+
+
+def test_missing_native_checks_fail_loudly(L, monkeypatch, tmp_path):
+    monkeypatch.setattr(api, "_binding", None)
+    monkeypatch.setattr(api, "_PKG", str(tmp_path))
+    with pytest.raises(RuntimeError, match="missing"):
+        api._native()
+
+
+def test_kinds_match_the_entry_points(L):
+    """One kind and one name per pointer argument of each entry point."""
+    for fn, kinds, names in (
+            (L.losa_quantize_prefix, "KK88ssm", 7), (L.losa_append_block_quant, "bb88ssm", 7),
+            (L.losa_dequantize_prefix, "88ssKK", 6),
+            (L.losa_dense_prefix_quant, "Q88ssbbOLOlW", len(api._DENSE_NAMES)),
+            (L.losa_step_quant, "QQ88ssMbbOLOlapuW", len(api._STEP_NAMES))):
+        ws = "W" in kinds
+        assert len(kinds) == names == len(fn.argtypes) - 2 - ws
+        for k in kinds:
+            api._expected(S(), k)
 
 
 # ---- the model the GPU tests compare with ---------------------------------
