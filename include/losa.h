@@ -354,8 +354,8 @@ int losa_dense_prefix_quant(const losa_shape* shape, const void* q, const void* 
 
 /*
  * losa_step and losa_step_ref over a quantised prefix: the same selection (from
- * page_meta) and the same results, with the selected pages read as codes and
- * scales.  Workspace: LOSA_WS_STEP.
+ * page_meta) and, up to the order of sums, the same results, with the selected
+ * pages read as codes and scales.  Workspace: LOSA_WS_STEP.
  */
 int losa_step_quant(const losa_shape* shape, const void* q_cur, const void* q_prev,
                     const void* k8, const void* v8, const float* k_scale, const float* v_scale,

@@ -10,8 +10,8 @@
 // their order) and scaled once.
 //
 // All three kernels give one warp to one page of K or V: it reads the page
-// once with 16-byte loads, all of them in flight, reduces its largest magnitude
-// in registers, and writes codes, scale and record.  The bound is HBM.
+// once, all of its loads in flight, reduces its largest magnitude in registers,
+// and writes codes, scale and record.  The bound is HBM.
 #include "e4m3.cuh"
 #include "losa_common.cuh"
 
@@ -63,12 +63,44 @@ __device__ __forceinline__ int encode_page(const float (&x)[8][8], int n, uint2 
   return e;
 }
 
-// The metadata record and norms of page p of group sg from its codes (laid out
-// as in encode_page) and its scale 2^e.
+// The metadata record and norms of page p of group sg: lane (h = lane / 16,
+// c = lane % 16) has channels 8c .. of kmin (h = 0) or kmax (h = 1).
+template <int DT>
+__device__ __forceinline__ void store_record(const float (&v)[8], void* meta, int sg, int p,
+                                             const Dims& d) {
+  const int lane = threadIdx.x & 31, h = lane >> 4, c = lane & 15;
+  // this half's norm, every operation rounded up
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = __fmaf_ru(v[j], v[j], sum);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum = __fadd_ru(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+  if (c == 0) {
+    float* nrm = reinterpret_cast<float*>(static_cast<char*>(meta) + meta_norm_offset(d));
+    nrm[(static_cast<size_t>(sg) * meta_norm_stride(d) + p) * 2 + h] = __fsqrt_ru(sum);
+  }
+  char* rec = static_cast<char*>(meta) + (static_cast<size_t>(sg) * d.Pc + p) * (2 * kD * d.esz);
+  if (DT == LOSA_BF16) {
+    // four significant bits and an exponent >= -109: exact in bf16
+    uint4 w;
+    w.x = (__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u);
+    w.y = (__float_as_uint(v[2]) >> 16) | (__float_as_uint(v[3]) & 0xffff0000u);
+    w.z = (__float_as_uint(v[4]) >> 16) | (__float_as_uint(v[5]) & 0xffff0000u);
+    w.w = (__float_as_uint(v[6]) >> 16) | (__float_as_uint(v[7]) & 0xffff0000u);
+    *reinterpret_cast<uint4*>(rec + meta_swz(h * 2u * kD + 16u * c, p)) = w;
+  } else {
+    *reinterpret_cast<float4*>(rec + meta_swz(h * 4u * kD + 32u * c, p)) =
+        make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(rec + meta_swz(h * 4u * kD + 32u * c + 16u, p)) =
+        make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// The same from the page's codes (laid out as in encode_page) and its scale 2^e.
 template <int DT>
 __device__ __forceinline__ void code_record(const uint2 (&codes)[8], int n, int e, void* meta,
                                             int sg, int p, const Dims& d) {
-  const int lane = threadIdx.x & 31, h = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 31, h = lane >> 4;
   // min/max of the codes as fp16 pairs (exact); a half-warp without a token
   // (n = 1) starts from the other one's
   uint32_t lo[4], hi[4];
@@ -101,33 +133,88 @@ __device__ __forceinline__ void code_record(const uint2 (&codes)[8], int n, int 
     v[2 * q] = f.x * s;
     v[2 * q + 1] = f.y * s;
   }
-  // this half's norm, every operation rounded up
-  float sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sum = __fmaf_ru(v[j], v[j], sum);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum = __fadd_ru(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-  if (c == 0) {
-    float* nrm = reinterpret_cast<float*>(static_cast<char*>(meta) + meta_norm_offset(d));
-    nrm[(static_cast<size_t>(sg) * meta_norm_stride(d) + p) * 2 + h] = __fsqrt_ru(sum);
-  }
-  char* rec = static_cast<char*>(meta) + (static_cast<size_t>(sg) * d.Pc + p) * (2 * kD * d.esz);
-  if (DT == LOSA_BF16) {
-    // four significant bits and an exponent >= -109: exact in bf16
-    uint4 w;
-    w.x = (__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u);
-    w.y = (__float_as_uint(v[2]) >> 16) | (__float_as_uint(v[3]) & 0xffff0000u);
-    w.z = (__float_as_uint(v[4]) >> 16) | (__float_as_uint(v[5]) & 0xffff0000u);
-    w.w = (__float_as_uint(v[6]) >> 16) | (__float_as_uint(v[7]) & 0xffff0000u);
-    *reinterpret_cast<uint4*>(rec + meta_swz(h * 2u * kD + 16u * c, p)) = w;
-  } else {
-    *reinterpret_cast<float4*>(rec + meta_swz(h * 4u * kD + 32u * c, p)) =
-        make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(rec + meta_swz(h * 4u * kD + 32u * c + 16u, p)) =
-        make_float4(v[4], v[5], v[6], v[7]);
-  }
+  store_record<DT>(v, meta, sg, p, d);
 }
 
+// ---- whole pages: the elements stay in their own type until they are encoded
+__device__ __forceinline__ uint32_t bf2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The eight elements of one token that a lane holds.
+template <int DT>
+struct Row8;
+template <>
+struct Row8<LOSA_BF16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const void* base, size_t idx) {
+    w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + idx));
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void minmax(Row8& lo, Row8& hi) const {
+    lo.w = make_uint4(bf2_min(lo.w.x, w.x), bf2_min(lo.w.y, w.y), bf2_min(lo.w.z, w.z), bf2_min(lo.w.w, w.w));
+    hi.w = make_uint4(bf2_max(hi.w.x, w.x), bf2_max(hi.w.y, w.y), bf2_max(hi.w.z, w.z), bf2_max(hi.w.w, w.w));
+  }
+  __device__ __forceinline__ void absmax(Row8& m) const {
+    constexpr uint32_t k = 0x7fff7fffu;
+    m.w = make_uint4(bf2_max(m.w.x, w.x & k), bf2_max(m.w.y, w.y & k), bf2_max(m.w.z, w.z & k),
+                     bf2_max(m.w.w, w.w & k));
+  }
+  __device__ __forceinline__ Row8 other_half() const {
+    Row8 r;
+    r.w = make_uint4(__shfl_xor_sync(0xffffffffu, w.x, 16), __shfl_xor_sync(0xffffffffu, w.y, 16),
+                     __shfl_xor_sync(0xffffffffu, w.z, 16), __shfl_xor_sync(0xffffffffu, w.w, 16));
+    return r;
+  }
+};
+template <>
+struct Row8<LOSA_F32> {
+  float v[8];
+  __device__ __forceinline__ void load(const void* base, size_t idx) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + idx);
+    const float4 a = __ldcs(p), b = __ldcs(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+  }
+  __device__ __forceinline__ void minmax(Row8& lo, Row8& hi) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo.v[i] = fminf(lo.v[i], v[i]);
+      hi.v[i] = fmaxf(hi.v[i], v[i]);
+    }
+  }
+  __device__ __forceinline__ void absmax(Row8& m) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m.v[i] = fmaxf(m.v[i], fabsf(v[i]));
+  }
+  __device__ __forceinline__ Row8 other_half() const {
+    Row8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = __shfl_xor_sync(0xffffffffu, v[i], 16);
+    return r;
+  }
+};
+
+// Rounding to a code keeps the order, so the codes' min and max over a page are
+// the codes of the elements' min and max: K needs no second look at its codes.
 template <int DT>
 __global__ void __launch_bounds__(kQWarps * 32)
     quantize_kernel(const void* __restrict__ K, const void* __restrict__ V,
@@ -144,18 +231,63 @@ __global__ void __launch_bounds__(kQWarps * 32)
   const int n = min(kPS, L - p * kPS);
   const size_t e0 = (static_cast<size_t>(sg) * d.Lc + p * kPS) * kD + kChunk * c;
   const void* src = isk ? K : V;
-  float x[8][8];
+  Row8<DT> x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)  // (a token past the end reads the page's first one instead)
-    ld8<DT>(src, e0 + static_cast<size_t>(2 * i + h < n ? 2 * i + h : 0) * kD, x[i]);
-  uint2 codes[8];
-  const int e = encode_page(x, n, codes);
+  for (int i = 0; i < 8; ++i)  // (a token past the end: the page's first one again)
+    x[i].load(src, e0 + static_cast<size_t>(2 * i + h < n ? 2 * i + h : 0) * kD);
+  const bool rec = isk && meta;
+  Row8<DT> lo = x[0], hi = x[0];
+  float amax = 0.f;
+  {
+    Row8<DT> m;
+    if (rec) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) x[i].minmax(lo, hi);
+      const Row8<DT> a = lo.other_half(), b = hi.other_half();
+      a.minmax(lo, hi);
+      b.minmax(lo, hi);
+    }
+    float f[8];
+    if (rec) {
+      lo.floats(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));  // (fmaxf drops a NaN)
+      hi.floats(f);
+    } else {
+      m = x[0];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i].absmax(m);
+      m.floats(f);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+  }
+  // non-negative floats are ordered like their bits
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  const int e = page_scale_exp(amax);
+  const float inv = exp2_int(-e);
   uint8_t* dst = isk ? k8 : v8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (2 * i + h < n) *reinterpret_cast<uint2*>(dst + e0 + (2 * i + h) * kD) = codes[i];
+  for (int i = 0; i < 8; ++i) {
+    float f[8];
+    x[i].floats(f);
+    uint2 w;
+    w.x = e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+    w.y = e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+    if (2 * i + h < n) *reinterpret_cast<uint2*>(dst + e0 + (2 * i + h) * kD) = w;
+  }
   if (lane == 0) (isk ? ks : vs)[static_cast<size_t>(sg) * d.Pc + p] = exp2_int(e);
-  if (isk && meta) code_record<DT>(codes, n, e, meta, sg, p, d);
+  if (rec) {
+    float f[8], v[8];
+    if (h) hi.floats(f);
+    else lo.floats(f);
+    const float4 a = e4m3x4_to_f32(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv));
+    const float4 b = e4m3x4_to_f32(e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
+    const float s = exp2_int(e);
+    v[0] = a.x * s, v[1] = a.y * s, v[2] = a.z * s, v[3] = a.w * s;
+    v[4] = b.x * s, v[5] = b.y * s, v[6] = b.z * s, v[7] = b.w * s;
+    store_record<DT>(v, meta, sg, p, d);
+  }
 }
 
 // One warp per touched page of K or V (pages L/ps .. (L+B-1)/ps): the page's

@@ -2189,12 +2189,14 @@ struct Taker {
   }
 };
 
-// clusters of 8 and of 16 CTAs that can be resident at once (1 CTA per SM)
+// clusters of 8, 16, 4 and 2 CTAs that can be resident at once (1 CTA per SM)
 struct ClusterRoom {
-  int c8 = 0, c16 = 0;
+  int c8 = 0, c16 = 0, c4 = 0, c2 = 0;
 };
 
-bool plan_step(const Dims& d, StepParams* prm, int max_dyn, const ClusterRoom& room) {
+// csize: CTAs per cluster at most (0: the default plan).
+bool plan_step(const Dims& d, StepParams* prm, int max_dyn, const ClusterRoom& room,
+               int csize = 0) {
   *prm = StepParams();
   prm->d = d;
   const bool bf = d.esz == 2;
@@ -2215,6 +2217,10 @@ bool plan_step(const Dims& d, StepParams* prm, int max_dyn, const ClusterRoom& r
   int C = std::max((d.P + prm->tile - 1) / prm->tile, (R + 15) / 16);
   C = std::max(1, std::min(cmax, C));
   if (R == 0) C = 1;
+  if (csize > 0) {
+    if (csize < (R + 15) / 16) return false;
+    C = std::min(C, csize);
+  }
   prm->C = C;
   prm->cp = align_up((d.P + C - 1) / C, 8);
   // candidate lists: entries per row left for the merge, and room for the
@@ -2241,7 +2247,8 @@ bool plan_step(const Dims& d, StepParams* prm, int max_dyn, const ClusterRoom& r
   const int MW = (R + 31) / 32;
   // one wave: every cluster resident at once (the next launch may then be
   // scheduled from the start)
-  prm->early = NG <= (C > kMaxCombineCtas ? room.c16 : room.c8);
+  prm->early = NG <= (C > kMaxCombineCtas ? room.c16 : csize > 0 && C <= 2 ? room.c2
+                      : csize > 0 && C <= 4 ? room.c4 : room.c8);
 
   // the largest plan that fits, with at least 4 ring stages when any plan
   // allows it: most pages per score chunk, then most union pages in flight,
@@ -2380,6 +2387,8 @@ int ensure_attributes(int* max_dyn, ClusterRoom* room) {
     g_attr_dyn[dev] = dyn;
     g_attr_room[dev].c8 = room_for(kMaxCombineCtas, dyn);
     g_attr_room[dev].c16 = room_for(kMaxClusterCtas, dyn);
+    g_attr_room[dev].c4 = room_for(4, dyn);
+    g_attr_room[dev].c2 = room_for(2, dyn);
     g_attr_done[dev] = true;
   }
   *max_dyn = g_attr_dyn[dev];
@@ -2406,9 +2415,26 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
   int rc = ensure_attributes(&max_dyn, &room);
   if (rc != LOSA_OK) return rc;
   StepParams prm;
-  if (!plan_step(d, &prm, max_dyn, room) && !plan_step(d, &prm, max_dyn, ClusterRoom()))
-    return LOSA_ERR_UNSUPPORTED;
   const long long NG = static_cast<long long>(d.S) * d.Hkv;
+  // 8-bit prefix, more clusters than run at once: a wave of clusters takes about
+  // 22 us and 1.1 us for each ring stage of pages that a CTA scores (64K prefix:
+  // 8 stages, 32 us), so clusters of 4 or 2 CTAs, of which two or four times as
+  // many run at once, can be faster.
+  bool planned = false;
+  if (d.quant && room.c8 > 0 && NG > room.c8) {
+    int best = 0;
+    double best_us = 0;
+    for (int c : {8, 4, 2}) {
+      const int r = c == 8 ? room.c8 : c == 4 ? room.c4 : room.c2;
+      if (r < 1 || !plan_step(d, &prm, max_dyn, room, c == 8 ? 0 : c)) continue;
+      const double waves = static_cast<double>((NG + r - 1) / r);
+      const double us = waves * (22.0 + 1.1 * ((prm.cp + prm.tile - 1) / prm.tile));
+      if (best == 0 || us < best_us) best = c, best_us = us;
+    }
+    planned = best != 0 && plan_step(d, &prm, max_dyn, room, best == 8 ? 0 : best);
+  }
+  if (!planned && !plan_step(d, &prm, max_dyn, room) && !plan_step(d, &prm, max_dyn, ClusterRoom()))
+    return LOSA_ERR_UNSUPPORTED;
   if (NG > 65535) return LOSA_ERR_UNSUPPORTED;
   prm.qc = q_cur;
   prm.qp = q_prev;

@@ -262,6 +262,35 @@ def test_step_equals_the_step_over_the_read_back_prefix(dtype, lens, Hkv, G, B, 
         assert torch.equal(ra, rb) and not torch.equal(ra, q[0])
 
 
+@pytest.mark.parametrize("dtype,lens,Hkv,G,B,A,budget,flags", [
+    ("bf16", [3000, 2999, 1, 1700], 8, 4, 16, 4, 256, 0), ("bf16", [2500] * 8, 8, 4, 32, 8, 256, 0),
+    ("f32", [1500] * 6, 4, 2, 8, 3, 64, 0), ("bf16", [900] * 5, 8, 8, 16, 8, 64, UNION),
+    ("bf16", [40] * 20, 2, 1, 1, 1, 16, 0)])
+def test_step_with_more_groups_than_run_at_once(dtype, lens, Hkv, G, B, A, budget, flags):
+    """More (sequence, KV head) groups than clusters of 8 fit the GPU: the 8-bit step takes
+    smaller clusters, so sums run in another order than in the step over the read-back
+    prefix.  Selections are the same; each of the two carries weights within 2^-16 of the
+    exact ones (two bf16 parts) and fp32 sums, so they differ by at most 2 * 2^-15 max|v|,
+    and the log-normalisers by 2^-15."""
+    sh, cache, meta, q, kb, vb = inputs(dtype, lens, Hkv, G, B, max(lens) + 3, sum(lens) + A, A=A,
+                                        budget=budget, flags=flags)
+    K, V = (torch.full((len(lens), Hkv, sh.capacity, 128), float("nan"), dtype=sh.torch_dtype,
+                       device=DEV) for _ in range(2))
+    api.dequantize_prefix(sh, *cache, K, V)
+    o, l = state_of(sh, 3)
+    a = gpu_step_quant(sh, q[1], q[0], cache, meta, kb, vb, o.clone(), l.clone())
+    b = gpu_step(sh, q[1], q[0], K, V, meta, kb, vb, o.clone(), l.clone())
+    assert api.read_device_status(a["ws"]) == api.LOSA_OK
+    for key in ("active_idx", "page_idx", "union_count"):
+        assert torch.equal(a[key], b[key]), key
+    vmax = max(torch.nan_to_num(V).abs().max().item(), vb.abs().max().item(), o.abs().max().item())
+    for key in ("o_p", "out", "l_p", "lse"):
+        tol = 2.0 ** -14 * vmax if key in ("o_p", "out") else 2.0 ** -15
+        assert (a[key] - b[key]).abs().max().item() <= tol, key
+    again = gpu_step_quant(sh, q[1], q[0], cache, meta, kb, vb, o.clone(), l.clone())
+    assert all(torch.equal(a[key], again[key]) for key in KEYS)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_step_other_scales(dtype):
     """Scales that are no powers of two, against the oracle on the read-back prefix (its
