@@ -149,12 +149,19 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     first = static_cast<size_t>(c0) + sg;
     nparts = line_cta_of(x0 + nt - 1, total, n) - c0 + 1;
   }
+  // one warp per row: row blockIdx.y * kFinishWarps + warp of head h; its
+  // attention over the block's own keys while the split kernel drains
+  const int t = blockIdx.y * kFinishWarps + warp;
+  float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+  float Ls = 0.f;
+  if (t < d.B) {
+    const float4 q = ld4(Q, (static_cast<size_t>(sh) * d.B + t) * kD + 4 * lane, d.dtype);
+    suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
+  }
   // launched behind the split kernel (programmatic dependent launch): its
   // partials are read only after it has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // one warp per row: rows blockIdx.y * kFinishWarps + warp of head h
-  for (int t = blockIdx.y * kFinishWarps + warp;
-       t < min(d.B, (blockIdx.y + 1) * kFinishWarps); t += kFinishWarps) {
+  if (t < d.B) {
     const size_t row = static_cast<size_t>(sh) * d.B + t;
     const int r = (h - g * d.G) * d.B + t;
     // merge the prefix partials (base-2 units) of every split in one pass,
@@ -205,10 +212,6 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     const float Lp = (M + __log2f(lsum)) * kLn2;
     *reinterpret_cast<float4*>(o_p + row * kD + 4 * lane) = op;
     if (lane == 0) l_p[row] = Lp;
-    const float4 q = ld4(Q, row * kD + 4 * lane, d.dtype);
-    float4 os;
-    float Ls;
-    suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
     float4 o;
     float L;
     lse_merge(op, Lp, os, Ls, o, L);

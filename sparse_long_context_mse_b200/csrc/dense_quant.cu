@@ -567,7 +567,8 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           for (int w = 1; w < 4; ++w) m = fmaxf(m, xg[w * CW + lane]);
           const float old = -nm[c0 + lane];
           const bool move = m > old + kRefMove || (old == -INFINITY && m > old);
-          const float ref = move ? m - kRefTop : old;
+          // (exponents so large that 11 is lost in their rounding: m itself)
+          const float ref = !move ? old : fabsf(m) < 1048576.f ? m - kRefTop : m;
           ag[lane] = move ? exp2f(old - ref) : 1.f;
           nm[c0 + lane] = -ref;
         }

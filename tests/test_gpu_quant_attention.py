@@ -134,6 +134,32 @@ def test_dense_zero_and_tiny_queries():
     dense_case(sh, cache, q0, kb, vb)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dense_huge_scores(dtype):
+    """Scores so large that a unit is lost in their rounding: the softmax is one key, its
+    value the output, and the log-normaliser its score (to 2^-20 of it: a product of
+    exact numbers and three roundings)."""
+    sh, cache, _, q, kb, vb = inputs(dtype, [700], 2, 2, 8, seed=52)
+    k = torch.zeros(1, 2, 700, 128)
+    k[:, :, 333] = 2.0 ** 24
+    k[:, :, 500] = 2.0 ** 10
+    v = torch.randn(1, 2, 700, 128, generator=torch.Generator().manual_seed(3))
+    api.quantize_prefix(sh, k.to(sh.torch_dtype).to(DEV), v.to(sh.torch_dtype).to(DEV), *cache)
+    qq = torch.full_like(q[0], 8.0)
+    got = gpu_dense_quant(sh, qq, cache, kb, vb)
+    ref, _ = dense_reference(sh, qq, *cache, kb, vb)
+    want = read_back(cache[1], cache[3])[0, :, 333]
+    for key in ("o_p", "out"):
+        g = got[key].double().reshape(2, 16, 128)
+        assert (g - want[:, None]).abs().max().item() <= 2.0 ** -20 * 8
+    for key in ("l_p", "lse"):
+        assert ((got[key].cpu().double() - ref[key]) / ref[key]).abs().max().item() <= 2.0 ** -20
+    # and so small that all keys weigh the same
+    got = gpu_dense_quant(sh, qq * 2.0 ** -60, cache, kb, vb)
+    ref, _ = dense_reference(sh, qq * 2.0 ** -60, *cache, kb, vb)
+    assert (got["o_p"].cpu().double() - ref["o_p"]).abs().max().item() <= 2.0 ** -18 * 5
+
+
 def test_dense_matches_the_pass_over_the_read_back_prefix():
     sh, cache, _, q, kb, vb = inputs("bf16", [4000], 2, 4, 16, seed=61)
     got = gpu_dense_quant(sh, q[0], cache, kb, vb)
