@@ -337,26 +337,30 @@ __device__ __forceinline__ void tile_attend(TileAcc& t, const char* q16, const c
   }
 }
 
-// 8-bit prefix: one warp turns a gathered page of K or V -- 16 x 128 e4m3 codes
-// in the last 2 KB of its slot -- into the slot's element type, in place (every
-// lane reads its codes before any lane stores).  bf16: the codes' own values in
-// the kv_off<true> layout (exact; the page scale stays a factor of the scores or
-// the weights); fp32: code * scale, plain rows.  Rows >= ntok become zero.
+// 8-bit prefix: one warp turns a gathered page -- 16 x 128 e4m3 codes each of K
+// and V, in the last 2 KB of their slots -- into the slots' element type, in
+// place (every lane reads its codes before any lane stores).  bf16: the codes'
+// own values in the kv_off<true> layout (exact; the page scales stay factors of
+// the scores and the weights); fp32: code * scale, plain rows.  Rows >= ntok
+// become zero.
 template <int DT>
-__device__ __forceinline__ void expand_page(char* slot, int ntok, float scale) {
+__device__ __forceinline__ void expand_page(char* kslot, char* vslot, int ntok, float2 scale) {
   const int lane = threadIdx.x & 31;
   constexpr int raw0 = kPS * kD * ((DT == LOSA_BF16 ? 2 : 4) - 1);
-  uint4 raw[4];
+  uint4 raw[8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = lane + 32 * q;  // row e / 8, channels 16 (e % 8) ..
-    raw[q] = (e >> 3) < ntok ? *reinterpret_cast<const uint4*>(slot + raw0 + e * 16)
-                             : make_uint4(0u, 0u, 0u, 0u);
+  for (int q = 0; q < 8; ++q) {
+    const int e = lane + 32 * (q & 3);  // row e / 8, channels 16 (e % 8) ..
+    raw[q] = (e >> 3) < ntok
+                 ? *reinterpret_cast<const uint4*>((q < 4 ? kslot : vslot) + raw0 + e * 16)
+                 : make_uint4(0u, 0u, 0u, 0u);
   }
   __syncwarp();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int e = lane + 32 * q, row = e >> 3;
+  for (int q = 0; q < 8; ++q) {
+    const int e = lane + 32 * (q & 3), row = e >> 3;
+    char* slot = q < 4 ? kslot : vslot;
+    const float sc = q < 4 ? scale.x : scale.y;
     const uint32_t w[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
     if (DT == LOSA_BF16) {
       uint32_t b[8];
@@ -375,7 +379,7 @@ __device__ __forceinline__ void expand_page(char* slot, int ntok, float scale) {
       for (int i = 0; i < 4; ++i) {
         const float4 f = e4m3x4_to_f32(w[i]);
         *reinterpret_cast<float4*>(slot + row * 512 + (e & 7) * 64 + i * 16) =
-            make_float4(f.x * scale, f.y * scale, f.z * scale, f.w * scale);
+            make_float4(f.x * sc, f.y * sc, f.z * sc, f.w * sc);
       }
     }
   }
@@ -1811,23 +1815,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nbat > 0) issue(0);
     if (nbat > 1) issue(1);
   }
-  if (Q8) {  // (read after the next block barrier)
-#pragma unroll 1
-    for (int i = tid; i < nlp; i += kThreads) {
-      const size_t o = static_cast<size_t>(sg) * d.Pc + lpages[i];
-      psc[i] = make_float2(prm.ks[o], fmaxf(prm.vs[o], kMinScale));
-    }
-  }
+  // the pages' scales: on their way while the suffix is computed, in shared
+  // memory before the block barrier after it
+  auto page_scales = [&](int i) {
+    const size_t o = static_cast<size_t>(sg) * d.Pc + lpages[i];
+    return make_float2(prm.ks[o], prm.vs[o]);
+  };
+  float2 my_scales = make_float2(0.f, 0.f);
+  if (Q8 && tid < nlp) my_scales = page_scales(tid);
   // the pages of batch bt have landed: their codes become elements
   auto expand = [&](int bt) {
     const int b0 = bt * prm.ngp, nb = min(prm.ngp, nlp - b0);
     char* bufp = ring + (bt & 1) * prm.ngp * 2 * pbytes;
 #pragma unroll 1
-    for (int u = warp; u < 2 * nb; u += kWarps) {
-      const int i = b0 + (u >> 1);
-      expand_page<DT>(bufp + u * pbytes, min(kPS, Ls - lpages[i] * kPS),
-                      (u & 1) ? psc[i].y : psc[i].x);
-    }
+    for (int i = warp; i < nb; i += kWarps)
+      expand_page<DT>(bufp + 2 * i * pbytes, bufp + (2 * i + 1) * pbytes,
+                      min(kPS, Ls - lpages[b0 + i] * kPS), psc[b0 + i]);
     fence_async_smem();  // before a later batch's copies land on these stores
   };
   LOSA_PHASE(12);
@@ -1910,6 +1913,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (prm.out_lse && lane == 0) prm.out_lse[grow] = L;
         }
       }
+    }
+  }
+  if (Q8) {
+#pragma unroll 1
+    for (int i = tid; i < nlp; i += kThreads) {
+      const float2 sc = i == tid ? my_scales : page_scales(i);
+      psc[i] = make_float2(sc.x, fmaxf(sc.y, kMinScale));
     }
   }
   __syncthreads();

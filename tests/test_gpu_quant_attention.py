@@ -80,6 +80,26 @@ def test_dense_long(dtype, G, B):
     dense_case(sh, cache, q[0], kb, vb)
 
 
+@pytest.mark.parametrize("S,Hkv,G,B", [(70, 1, 4, 4), (33, 3, 2, 1), (150, 2, 1, 1)])
+def test_dense_many_sequences(S, Hkv, G, B):
+    """More sequences than a warp has lanes, and more KV heads than CTAs: the CTAs' places
+    among the tiles come from sums over all lengths."""
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(1, 700, (S,), generator=g).tolist()
+    lens[S // 2] = 1500
+    sh, cache, _, q, kb, vb = inputs("bf16", lens, Hkv, G, B, cap=1511, seed=S)
+    dense_case(sh, cache, q[0], kb, vb)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dense_rows_of_different_sizes(dtype):
+    """Query rows and parts of rows of very different sizes, in one head."""
+    sh, cache, _, q, kb, vb = inputs(dtype, [900], 2, 4, 16, seed=32)
+    g = torch.Generator().manual_seed(33)
+    size = torch.exp2(torch.randint(-24, 3, (1, 8, 16, 1), generator=g).float())
+    dense_case(sh, cache, (q[0].cpu().float() * size).to(sh.torch_dtype).to(DEV), kb, vb)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_dense_growing_scores(dtype):
     """Scores that rise along the prefix, so that the running maximum moves many times,
