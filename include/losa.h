@@ -290,8 +290,8 @@ int losa_step_ref(const losa_shape* shape, const void* q_cur, void* q_ref,
  * holds, code * scale, so that the bound stays a bound of what is attended to.
  *
  * The calls that read a cache take any finite scales, also ones written by
- * another program, of which the V scales are >= 0 (a V scale below 2^-100 is
- * taken as 2^-100).  Scales and codes of pages and tokens past a sequence's
+ * another program, of which the V scales are >= 0 (the attention calls take a V
+ * scale below 2^-100 as 2^-100).  Scales and codes of pages and tokens past a sequence's
  * length are never used, whatever they hold, and never written.
  * Scale arrays need the alignment of a float only (a layer's slice of a larger
  * array), the other buffers 16 bytes as everywhere. */
@@ -355,7 +355,9 @@ int losa_dense_prefix_quant(const losa_shape* shape, const void* q, const void* 
 /*
  * losa_step and losa_step_ref over a quantised prefix: the same selection (from
  * page_meta) and, up to the order of sums, the same results, with the selected
- * pages read as codes and scales.  Workspace: LOSA_WS_STEP.
+ * pages read as codes and scales.  Workspace: LOSA_WS_STEP.  The pages' scales
+ * are kept on chip too: of the largest steps that losa_step takes (hundreds of
+ * pages for each CTA) a few are refused here, LOSA_ERR_UNSUPPORTED.
  */
 int losa_step_quant(const losa_shape* shape, const void* q_cur, const void* q_prev,
                     const void* k8, const void* v8, const float* k_scale, const float* v_scale,

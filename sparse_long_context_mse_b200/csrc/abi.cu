@@ -150,7 +150,10 @@ int make_dims(const losa_shape* sh, int which, Dims* d) {
     // A CTA that crosses from one KV head into the next loses about four tiles'
     // time (its pipeline drains, the next queries are staged).  Sequences of one
     // length can be cut at KV heads, with a whole number of CTAs for each: better
-    // while the longest range grows by less than that.
+    // while the longest range grows by less than that.  Measured, even ranges and
+    // cut ones: 8 KV heads, 64 rows: 64K prefix 45.7 and 43.1 us, 8K 19.0 and 16.7;
+    // 8 sequences of 32K, 128 rows, where the cut makes a range 34 tiles longer:
+    // 285 and 318 us, not cut.
     const long long per = d->line_ctas / static_cast<long long>(SG);
     if (!d->lens && per > 0) {
       const long long nt = tiles / static_cast<long long>(SG);

@@ -123,6 +123,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
   const int Bpad = (d.B + kPS - 1) / kPS * kPS;
   float* Ksb = fsm;
   float* Vsb = fsm + Bpad * kD;
+  // one warp per row: row blockIdx.y * kFinishWarps + warp of head h
+  const int t = blockIdx.y * kFinishWarps + warp;
+  float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (t < d.B) q = ld4(Q, (static_cast<size_t>(sh) * d.B + t) * kD + 4 * lane, d.dtype);
   for (int e = threadIdx.x; e < Bpad * kD / 4; e += blockDim.x) {
     const int j = e / (kD / 4), c = (e % (kD / 4)) * 4;
     float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
@@ -149,15 +153,10 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     first = static_cast<size_t>(c0) + sg;
     nparts = line_cta_of(x0 + nt - 1, total, n) - c0 + 1;
   }
-  // one warp per row: row blockIdx.y * kFinishWarps + warp of head h; its
-  // attention over the block's own keys while the split kernel drains
-  const int t = blockIdx.y * kFinishWarps + warp;
+  // the row's attention over the block's own keys while the split kernel drains
   float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
   float Ls = 0.f;
-  if (t < d.B) {
-    const float4 q = ld4(Q, (static_cast<size_t>(sh) * d.B + t) * kD + 4 * lane, d.dtype);
-    suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
-  }
+  if (t < d.B) suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
   // launched behind the split kernel (programmatic dependent launch): its
   // partials are read only after it has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");

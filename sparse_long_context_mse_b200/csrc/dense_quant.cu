@@ -11,8 +11,8 @@
 // scales of the pages are: a page of small values that holds the weight keeps
 // its relative accuracy.
 //
-// What bounds it is HBM: 256 bytes per key and KV head, read once.  The work is
-// laid out so that nothing on the chip takes longer:
+// Its floor is HBM: 256 bytes per key and KV head, read once.  The work is laid
+// out so that little on the chip takes longer:
 //
 // * Keys are the rows of both products (M = 128, one tile), the G*B query rows
 //   are the columns (N = 16, 32 or 64; 128 rows take two CTAs that read the same
@@ -29,8 +29,8 @@
 //   transpose V codes out of shared memory (ldmatrix, bytes), widen them (exact)
 //   and store them as the A operand in TMEM, which costs 1/8 of the shared-memory
 //   traffic of an fp16 tile there; W goes through shared memory as the MN-major B.
-// * A softmax thread owns one key (TMEM lane) and half of the query columns: the
-//   page scales are constants of the thread, l is a sum in registers across tiles
+// * A softmax thread owns one key (TMEM lane) and 8 or 16 of the query columns:
+//   the page scales are constants of the thread, l is a sum in registers across tiles
 //   (joined over the lanes at the end), and no tile needs a maximum over the
 //   lanes: the reference moves only when some w would pass 2^15, which one
 //   barrier with a vote finds out.
@@ -39,6 +39,17 @@
 //   so O stays in it for one tile only and is summed in registers.
 // * All SMs get the same number of tiles, whatever the lengths and the number of
 //   KV heads (the line of tiles, losa_common.cuh).
+//
+// Measured, calls back to back (with the finish kernel; the floor at the copy
+// bandwidth of 6.45 TB/s): 8 KV heads, 64K prefix, 134 MB, floor 21 us: 16 rows
+// per KV head 31.6 us, 32 rows 34.0, 64 rows 43.1.  Up to 32 rows it is bound by
+// the loads (what is left of it with the softmax taken out takes 28 us: 23 for
+// the bytes, and a prologue and an end that no tile overlaps).  With 64 rows a
+// tile's 2000 cycles go to the softmax warps: 8192 weights, each scaled, voted
+// on, raised to a power of two and split in two fp16 numbers, some 5200 warp
+// instructions at 0.65 a cycle and scheduler, with no pipe above 40 % busy and
+// the tensor core at 40 %.  Eight sequences of 32K and 128 rows (two CTAs each
+// range), floor 85 us: 285 us, the same softmax.
 #include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
@@ -88,9 +99,11 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
 // NR: query columns (MMA N); NQ: e4m3 parts of a query row (2: bf16, 6: fp32).
 template <int NR, int NQ>
 struct QPlan {
-  // A tile takes a softmax warp a chain of some 60 dependent waits and
-  // instructions per column, so the columns are spread over as many warps as the
-  // registers allow: 16 columns per thread at most.
+  // A tile is a chain of dependent waits and instructions for a softmax warp, and
+  // the longer the more columns it has, so the columns are spread over as many
+  // warps as the registers allow: 16 columns per thread at most (64 rows, 64K
+  // prefix: 51 us a pass with four warp groups, 59 with two; one CTA with 128
+  // columns in place of two with 64: 346 us for 8 x 32K, against 293).
   static constexpr int nwg = NR > 32 ? 4 : 2;            // softmax warp groups
   static constexpr int soft = nwg * 128;                 // .. threads
   static constexpr int threads = soft + 256;
@@ -103,7 +116,7 @@ struct QPlan {
   static constexpr int atom = kLineKeys * 128;           // 64 fp16 columns of W: 16 KB
   static constexpr int wbytes = 2 * atom;                // W and its remainder
   static constexpr int qbytes = NQ * NR * kD;
-  static constexpr int small = 3072;                     // barriers, row factors, exchange
+  static constexpr int small = 3 * 1024;                    // barriers, row factors, exchange
   static constexpr int room = kB200MaxDynSmem - small - qbytes - 2 * wbytes;
   static constexpr int st = room / (2 * kTileBytes) < 4 ? room / (2 * kTileBytes) : 4;
   static constexpr int nbars = 7 + 4 * st;
@@ -149,9 +162,6 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
   using C = QPlan<NR, NQ>;
   constexpr int CW = C::cw, ST = C::st, NA = C::na, NS = C::soft, W0 = NS / 32;
   extern __shared__ __align__(1024) char sm[];
-  // the finish kernel may be scheduled now; it waits for this grid's
-  // completion before it reads a partial
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (su32(sm) & 1023u) {  // (the swizzled tiles; dynamic shared memory starts at 1 KB)
     if (threadIdx.x == 0) atomicCAS(status, 0, LOSA_ERR_DEVICE_BOUNDS);
     return;
@@ -180,13 +190,26 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rows = d.G * d.B, r0 = blockIdx.y * NR, nrows = min(NR, rows - r0);
 
+  if (tid == 0) {
+    for (int i = 0; i < C::nbars; ++i)
+      mbar_init(&bars[i], i < 2 ? 2 : i < 4 ? 1 : i < 6 ? W0 + 4 : i == 6 ? W0 : i >= 7 + 3 * ST ? 4 : 1);
+    fence_mbar_init();
+    *s_fail = 0;
+  }
+  // launched with programmatic stream serialisation: nothing is read or written
+  // before the work queued ahead has completed.  Only then may the finish kernel
+  // be scheduled: it reads the queries and the block before its own wait
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1) tmem_alloc(tslot, C::cols);
   if (warp == 0) {
     // this CTA's range of the line, and where it starts
     long long before, all;
     line_sums(d, 0, before, all);
     const long long total = all * d.Hkv;
     const int n = line_ctas_used(d, total), b = blockIdx.x;
-    const long long x0 = b < n ? b * total / n : 0, x1 = b < n ? (b + 1) * total / n : 0;
+    const long long x0 = b < n ? line_div(b * total, n) : 0;
+    const long long x1 = b < n ? line_div((b + 1) * total, n) : 0;
     int s = 0;
     before = 0;
     if (d.lens) {
@@ -209,25 +232,19 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       }
     } else {
       const long long nt = (d.L + kLineKeys - 1) / kLineKeys;
-      s = static_cast<int>(x0 / (nt * d.Hkv));
+      s = static_cast<int>(line_div(x0, nt * d.Hkv));
       before = nt * s;
     }
     if (lane == 0) {
       const long long nt = line_tiles(d, s), y = x0 - before * d.Hkv;
       line[0] = static_cast<int>(x1 - x0);
       line[1] = s;
-      line[2] = static_cast<int>(y / nt);
-      line[3] = static_cast<int>(y % nt);
-      for (int i = 0; i < C::nbars; ++i)
-        mbar_init(&bars[i], i < 2 ? 2 : i < 4 ? 1 : i < 6 ? W0 + 4 : i == 6 ? W0 : i >= 7 + 3 * ST ? 4 : 1);
-      fence_mbar_init();
-      *s_fail = 0;
+      line[2] = static_cast<int>(line_div(y, nt));
+      line[3] = static_cast<int>(y - nt * line[2]);
     }
     if (b == 0 && blockIdx.y == 0)
       for (int i = lane; d.lens && i < d.S; i += 32)
         if (seq_len_bad(d, i)) atomicCAS(status, 0, LOSA_ERR_DEVICE_BOUNDS);
-    __syncwarp();
-    tmem_alloc(tslot, C::cols);
   }
   tc_fence_before();
   __syncthreads();
@@ -682,7 +699,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && *s_fail) atomicCAS(status, 0, LOSA_ERR_DEVICE_TIMEOUT);
-  if (warp == 0) tmem_dealloc(tb, C::cols);
+  if (warp == 1) tmem_dealloc(tb, C::cols);
 }
 
 template <int NR, int NQ>
@@ -704,9 +721,17 @@ int launch_partials(const Dims& d, const void* q, const void* k8, const void* v8
   if (make_byte_tmap(&kmap, k8, nrows, kLineKeys) != LOSA_OK ||
       make_byte_tmap(&vmap, v8, nrows, kLineKeys) != LOSA_OK)
     return record_cuda_error(cudaErrorInvalidValue);
-  fn<<<dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR), C::threads, C::smem, st>>>(
-      q, kmap, vmap, k_scale, v_scale, part, status, d);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cf = {};
+  cudaLaunchAttribute at[1];
+  cf.gridDim = dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR, 1);
+  cf.blockDim = dim3(C::threads, 1, 1);
+  cf.dynamicSmemBytes = C::smem;
+  cf.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cf.attrs = at;
+  cf.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cf, fn, q, kmap, vmap, k_scale, v_scale, part, status, d);
   return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
 }
 
@@ -742,11 +767,16 @@ extern "C" int losa_dense_prefix_quant(const losa_shape* shape, const void* q, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.off_part);
   int* status = reinterpret_cast<int*>(static_cast<char*>(workspace) + d.off_status);
+  // the fewest columns that hold the rows: what a tile costs beyond its loads
+  // grows with them (8 KV heads, 64K prefix, 16 rows: 31.6 us with 16 columns,
+  // 33.2 with 32, 40.6 with 64; fp32 36.1, 37.1, 46.4)
   const int r = d.G * d.B;
   auto* launch = d.dtype == LOSA_BF16 ? (r <= 16   ? launch_partials<16, 2>
                                          : r <= 32 ? launch_partials<32, 2>
                                                    : launch_partials<64, 2>)
-                                      : (r <= 16 ? launch_partials<16, 6> : launch_partials<64, 6>);
+                                      : (r <= 16   ? launch_partials<16, 6>
+                                         : r <= 32 ? launch_partials<32, 6>
+                                                   : launch_partials<64, 6>);
   rc = launch(d, q, k8, v8, k_scale, v_scale, part, status, st);
   if (rc != LOSA_OK) return rc;
   return launch_dense_finish(d, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, st);

@@ -22,12 +22,6 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
 }
-// The low two codes of `c` -> two fp16 values (exact), low half first.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(r) : "r"(c));
-  return r;
-}
 // Four codes -> fp16 pairs (codes 0, 1) and (codes 2, 3).
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t c, uint32_t& lo, uint32_t& hi) {
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"

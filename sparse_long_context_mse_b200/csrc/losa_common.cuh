@@ -166,12 +166,18 @@ __device__ __forceinline__ void line_sums(const Dims& d, int s, long long& befor
     before += __reduce_add_sync(0xffffffffu, i < s ? nt : 0);
   }
 }
+// Quotient of two non-negative numbers, in 32 bits when they fit (a 64-bit
+// division is a routine of a hundred instructions).
+__device__ __forceinline__ long long line_div(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<int>(a) / static_cast<int>(b);
+  return a / b;
+}
 // CTAs in use and the CTA whose range holds tile x: ranges [b T / n, (b+1) T / n).
 __device__ __forceinline__ int line_ctas_used(const Dims& d, long long total) {
   return static_cast<int>(total < d.line_ctas ? total : d.line_ctas);
 }
 __device__ __forceinline__ int line_cta_of(long long x, long long total, int n) {
-  return static_cast<int>(((x + 1) * n - 1) / total);
+  return static_cast<int>(line_div((x + 1) * n - 1, total));
 }
 
 __device__ __forceinline__ void set_status(void* ws, int code) {

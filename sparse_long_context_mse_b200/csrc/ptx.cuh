@@ -145,10 +145,6 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
-// An arrival at named barrier `id` of `n` threads, without waiting.
-__device__ __forceinline__ void bar_arrive(int id, int n) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
 // The same barrier, and whether `p` held for any of its threads.
 __device__ __forceinline__ bool bar_or(int id, int n, bool p) {
   uint32_t r;

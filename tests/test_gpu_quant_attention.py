@@ -245,6 +245,31 @@ def test_dense_captured_two_streams_and_replay():
     check_dense(out, *dense_reference(sh, q[0], *cache, kb, vb))
 
 
+@pytest.mark.parametrize("B", [1, 16])
+def test_dense_calls_queued_behind_the_kernels_that_write_their_inputs(B):
+    """Every call's queries, block and cache are written on the stream just before it, and
+    its results and workspace are used again just after it, with no wait between."""
+    cases = [inputs("bf16", [2500, 900], 2, 4, B, cap=2600, seed=97 + i) for i in range(6)]
+    sh = cases[0][0]
+    for other in cases[1:]:
+        sh_i = other[0]
+        assert [int(x) for x in sh_i._prefix_lens] == [int(x) for x in sh._prefix_lens]
+    cache = api.alloc_quant_prefix(sh, DEV)
+    q, kb, vb = (torch.empty_like(x) for x in (cases[0][3][0], *cases[0][4:]))
+    ws = api.alloc_workspace(sh, api.LOSA_WS_DENSE_QUANT, DEV)
+    out = alloc_state(sh, torch.device(DEV))
+    got = []
+    torch.cuda.synchronize()
+    for _, c, _, qs, k, v in cases:
+        for dst, src in zip((*cache, q, kb, vb), (*c, qs[0], k, v)):
+            dst.copy_(src)
+        for _ in range(2):  # (the second one's inputs are the first one's)
+            api.dense_prefix_quant(sh, q, *cache, kb, vb, out["o_p"], out["l_p"], out["out"], out["lse"], ws)
+        got.append({n: x.clone() for n, x in out.items()})
+    for r, (_, c, _, qs, k, v) in zip(got, cases):
+        check_dense(r, *dense_reference(sh, qs[0], *c, k, v))
+
+
 # ---------------------------------------------------------------------------
 # the step
 # ---------------------------------------------------------------------------
