@@ -659,19 +659,9 @@ int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const v
                         cudaStream_t st) {
   // behind the split kernel with programmatic dependent launch: the finish
   // CTAs stage the block's K/V while the split kernel drains
-  cudaLaunchConfig_t cf = {};
-  cudaLaunchAttribute at[1];
-  cf.gridDim = dim3(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps, 1);
-  cf.blockDim = dim3(kFinishWarps * 32, 1, 1);
-  cf.dynamicSmemBytes = 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float);
-  cf.stream = st;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cf.attrs = at;
-  cf.numAttrs = 1;
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cf, dense_finish_kernel, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
-  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
+  return launch_behind(dense_finish_kernel, dim3(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps),
+                       kFinishWarps * 32, 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float), st,
+                       q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
 }
 }  // namespace losa
 

@@ -721,18 +721,8 @@ int launch_partials(const Dims& d, const void* q, const void* k8, const void* v8
   if (make_byte_tmap(&kmap, k8, nrows, kLineKeys) != LOSA_OK ||
       make_byte_tmap(&vmap, v8, nrows, kLineKeys) != LOSA_OK)
     return record_cuda_error(cudaErrorInvalidValue);
-  cudaLaunchConfig_t cf = {};
-  cudaLaunchAttribute at[1];
-  cf.gridDim = dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR, 1);
-  cf.blockDim = dim3(C::threads, 1, 1);
-  cf.dynamicSmemBytes = C::smem;
-  cf.stream = st;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cf.attrs = at;
-  cf.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cf, fn, q, kmap, vmap, k_scale, v_scale, part, status, d);
-  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
+  return launch_behind(fn, dim3(d.line_ctas, (d.G * d.B + NR - 1) / NR), C::threads, C::smem, st, q,
+                       kmap, vmap, k_scale, v_scale, part, status, d);
 }
 
 }  // namespace

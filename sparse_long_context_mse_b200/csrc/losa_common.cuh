@@ -327,6 +327,25 @@ int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const v
                         const float* part, float* o_p, float* l_p, float* out, float* out_lse,
                         cudaStream_t st);
 int record_cuda_error(cudaError_t e);  // stores the message, returns LOSA_ERR_CUDA
+// Launch with programmatic stream serialisation: the grid may be scheduled while
+// the kernel ahead of it in the stream ends (or from where that one allows it), so
+// the kernel itself waits for it (griddepcontrol.wait) before it reads or writes
+// anything that others write or read.
+template <typename... P, typename... A>
+int launch_behind(void (*fn)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cf = {};
+  cudaLaunchAttribute at[1];
+  cf.gridDim = grid;
+  cf.blockDim = dim3(threads, 1, 1);
+  cf.dynamicSmemBytes = smem;
+  cf.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cf.attrs = at;
+  cf.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cf, fn, static_cast<P>(args)...);
+  return e == cudaSuccess ? LOSA_OK : record_cuda_error(e);
+}
 // 2-D tensor map over a [nrows][128] bf16 tensor at `base`, for
 // 128-byte-swizzled boxes of 64 channels x box_rows rows (rows past nrows
 // read as zero).  LOSA_OK, or LOSA_ERR_CUDA if the driver refuses it.
