@@ -354,8 +354,8 @@ int losa_dense_prefix_quant(const losa_shape* shape, const void* q, const void* 
 
 /*
  * losa_step and losa_step_ref over a quantised prefix: the same selection (from
- * page_meta) and, up to the order of sums, the same results, with the selected
- * pages read as codes and scales.  Workspace: LOSA_WS_STEP.  The pages' scales
+ * page_meta) and, up to rounding, the same results, with the selected pages
+ * read as codes and scales.  Workspace: LOSA_WS_STEP.  The pages' scales
  * are kept on chip too: of the largest steps that losa_step takes (hundreds of
  * pages for each CTA) a few are refused here, LOSA_ERR_UNSUPPORTED.
  */
