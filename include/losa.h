@@ -291,8 +291,10 @@ int losa_step_ref(const losa_shape* shape, const void* q_cur, void* q_ref,
  *
  * The calls that read a cache take any finite scales, also ones written by
  * another program, of which the V scales are >= 0 (the attention calls take a V
- * scale below 2^-100 as 2^-100).  Scales and codes of pages and tokens past a sequence's
- * length are never used, whatever they hold, and never written.
+ * scale below 2^-100 as 2^-100; the dense pass is accurate while the V scales
+ * of a KV head lie within 2^100 of each other).  Scales and codes of pages and
+ * tokens past a sequence's length are never used, whatever they hold, and never
+ * written.
  * Scale arrays need the alignment of a float only (a layer's slice of a larger
  * array), the other buffers 16 bytes as everywhere. */
 

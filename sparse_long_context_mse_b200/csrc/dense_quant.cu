@@ -18,12 +18,15 @@
 //   are the columns (N = 16, 32 or 64; 128 rows take two CTAs that read the same
 //   keys at the same time, the second time from L2): few query rows cost little.
 // * S^T = K8 Q^T runs on the codes as TMA brought them (kind::f8f6f4, e4m3 times
-//   e4m3): nothing converts K.  Q enters as a sum of e4m3 parts, each the
-//   rounding of what the parts before it left: a bf16 number has 8 significant
-//   bits, two parts of 4 hold it exactly; fp32 takes six, the last three 2^12
-//   times larger in an accumulator of their own.  Rows are scaled by a power of
-//   two to a maximum in [128, 256), so that two parts reach down to 2^-18 of the
-//   row's maximum (six: 2^-30).
+//   e4m3): nothing converts K.  Q enters as a sum of 8-bit parts, each the
+//   rounding of what the parts before it left, rows scaled by a power of two to a
+//   maximum in [128, 256).  A bf16 number has 8 significant bits: an e4m3 part
+//   holds 4, and what rounding to nearest leaves, -8 .. 8 units of the last place,
+//   has 3 at most, which is an e5m2 number.  So the two are exact down to 2^-13 of
+//   the row's maximum, and within 2^-21 of it below (an e4m3 second part, with its
+//   smaller range: 2^-17, and twice the results' error).  fp32 takes six e4m3
+//   parts, the last three 2^12 times larger in an accumulator of their own, within
+//   2^-29 of the row's maximum.
 // * O^T = V8^T W: W in fp16 (its rounding, and the rounding's remainder as a
 //   second fp16 operand: 22 bits), so V8 has to be fp16 too.  Four warps
 //   transpose V codes out of shared memory (ldmatrix, bytes), widen them (exact)
@@ -96,7 +99,7 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   return r;
 }
 
-// NR: query columns (MMA N); NQ: e4m3 parts of a query row (2: bf16, 6: fp32).
+// NR: query columns (MMA N); NQ: 8-bit parts of a query row (2: bf16, 6: fp32).
 template <int NR, int NQ>
 struct QPlan {
   // A tile is a chain of dependent waits and instructions for a softmax warp, and
@@ -293,6 +296,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
     } else if (warp == W0 + 5 && n > 0) {
       // ---- MMAs: the whole warp follows the loop, one elected thread issues
       constexpr uint32_t idS = umma_idesc_e4m3(128, NR);
+      constexpr uint32_t idS2 = umma_idesc_e4m3(128, NR, NQ == 2);
       constexpr uint32_t idO = umma_idesc_f16_bmn(128, NR);
       constexpr uint32_t idR = idO | (1u << 14);  // minus B: the remainder is stored negated
       const uint64_t dq = umma_desc(su32(qs), 16, 1024), dk = umma_desc(su32(kring), 16, 1024);
@@ -320,10 +324,11 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t ql = q_lo + (((a * (NQ / NA) + p) * NR * kD + k * 32) >> 4);
+              const uint32_t id = p > 0 ? idS2 : idS;
               if (p < NQ / NA - 1 || k > 0)
-                umma_e4m3<true>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, idS);
+                umma_e4m3<true>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, id);
               else
-                umma_e4m3<false>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, idS);
+                umma_e4m3<false>(me, ts + a * NR, kl + ((k * 32) >> 4), ql, kq_hi, id);
             }
         umma_commit_if(me, &bS[par]);
         umma_commit_if(me, &bKe[ks_]);
@@ -517,8 +522,11 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
 #pragma unroll
           for (int p = 0; p < NQ; ++p) {
             // (an infinite row maximum leaves no number: NaN, as its softmax)
-            const uint32_t w = amax < INFINITY ? e4m3x4(x.x, x.y, x.z, x.w) : 0x7f7f7f7fu;
+            const uint32_t w = amax == INFINITY          ? 0x7f7f7f7fu
+                               : NQ == 2 && p == 1 ? e5m2x4(x.x, x.y, x.z, x.w)
+                                                   : e4m3x4(x.x, x.y, x.z, x.w);
             *reinterpret_cast<uint32_t*>(dst + p * NR * kD) = w;
+            if (p == NQ - 1) break;
             const float4 y = e4m3x4_to_f32(w);
             const float f = NA == 2 && p == NQ / 2 - 1 ? kPartScale : 1.f;
             x = make_float4((x.x - y.x) * f, (x.y - y.y) * f, (x.z - y.z) * f, (x.w - y.w) * f);

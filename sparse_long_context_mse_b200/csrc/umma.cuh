@@ -145,9 +145,9 @@ __device__ __forceinline__ void tmem_st16x256_x4(uint32_t taddr, const float (&v
 
 // ---- 8-bit operands and operands in TMEM -----------------------------------
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B, both
-// K-major, shape M x N (K = 32 per instruction).
-__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// K-major, shape M x N (K = 32 per instruction).  b_e5m2: B is e5m2.
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N, bool b_e5m2 = false) {
+  return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B, A K-major
 // (in TMEM: lane = row, a 32-bit column holds two consecutive k), B MN-major.
@@ -169,7 +169,7 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 __device__ __forceinline__ uint32_t desc_lo(uint64_t d) { return static_cast<uint32_t>(d); }
 __device__ __forceinline__ uint32_t desc_hi(uint64_t d) { return static_cast<uint32_t>(d >> 32); }
-// D[tmem] (+)= A[smem] . B[smem], e4m3 operands.
+// D[tmem] (+)= A[smem] . B[smem], 8-bit operands.
 template <bool ACC>
 __device__ __forceinline__ void umma_e4m3(uint32_t me, uint32_t d_tmem, uint32_t a_lo,
                                           uint32_t b_lo, uint32_t hi, uint32_t idesc) {

@@ -139,18 +139,17 @@ def dense_bounds(T, small, vmax, lse):
     """Error bounds of the dense pass.  T: the largest sum of |terms| of a score; small:
     the largest (row maximum of |q|) * (sum of |k|), both in natural-log units.
 
-    * A query row is split into e4m3 parts: with two parts (bf16 queries) the split is
-      exact, with four (fp32) within 2^-16 of each element, but for elements near the
-      bottom of the row's range, where the error is at most 2^-18 of the row's maximum:
-      2^-16 T + 2^-18 small.
+    * A query row is split into 8-bit parts: bf16 rows into two, exact but for elements near
+      the bottom of the row's range, where the error is at most 2^-21 of the row's maximum
+      (2^-29 with the six parts of an fp32 row): 2^-21 small.
     * The score is summed in fp32 by the tensor core, at most 16 accumulations of
       2^-24 T (or one rounding per channel on CUDA cores: 128 of 2^-24 T): 2^-17 T.
     * Scaling the score and the exponential add 2^-20 in all.
     The sum d of these is the relative error of a weight.  Output: both the weighted sum
-    and the normaliser carry d, and the weights' rounding (2^-21), the 128 truncating
-    accumulations between drains (2^-24 each) and the merges add 2^-16 of max|v|.
-    Log-normaliser: d, and 2^-22 of its own size."""
-    d = 2.0 ** -16 * T + 2.0 ** -18 * small + 2.0 ** -17 * T + 2.0 ** -20
+    and the normaliser carry d, and the weights' rounding (2^-21), the truncating
+    accumulations of a tile (16 of 2^-24), the sums over tiles and the merges add 2^-16 of
+    max|v|.  Log-normaliser: d, and 2^-22 of its own size."""
+    d = 2.0 ** -21 * small + 2.0 ** -17 * T + 2.0 ** -20
     return {"o": (2 * d + 2.0 ** -16) * vmax, "l": d + 2.0 ** -20 + 2.0 ** -22 * lse}
 
 

@@ -144,6 +144,23 @@ def test_dense_other_scales(dtype):
     assert b.abs().max() < 1e-9 and (a - b).abs().max() <= 2.0 ** -14 * b.abs().max()
 
 
+@pytest.mark.parametrize("dtype,lens,Hkv,G,B,outlier", [
+    ("bf16", [3], 2, 1, 1, 1), ("bf16", [95, 60], 2, 8, 2, 1), ("bf16", [5000], 2, 4, 16, 1),
+    ("f32", [700], 2, 4, 8, 1), ("bf16", [400], 2, 4, 16, 60), ("f32", [400], 2, 4, 4, 60)])
+def test_dense_error_against_64_bits(dtype, lens, Hkv, G, B, outlier):
+    """Relative to the results' norm.  Scores of N(0, 1) queries and keys are below 2^3 in
+    base 2, those of rows with one channel 60 times larger below 2^7; the tensor core rounds
+    them (16 accumulations of at most 2^-24 of that: 2^-17 and 2^-13 in the worst case), and
+    the split of a row leaves 2^-21 of its maximum in a few channels, the less.  Independent
+    roundings add as squares: an eighth of the worst case, 2^-20 and 2^-16."""
+    sh, cache, _, q, kb, vb = inputs(dtype, lens, Hkv, G, B, seed=sum(lens))
+    q[0][..., 5] *= outlier
+    got, ref, _ = dense_case(sh, cache, q[0], kb, vb)
+    for key in ("o_p", "out"):
+        err = ((got[key].cpu().double() - ref[key]).norm() / ref[key].norm()).item()
+        assert err <= (2.0 ** -20 if outlier == 1 else 2.0 ** -16), (key, err)
+
+
 def test_dense_zero_and_tiny_queries():
     sh, cache, _, q, kb, vb = inputs("bf16", [500], 2, 4, 16, seed=51)
     q0 = q[0].clone()
