@@ -429,7 +429,7 @@ def _refuse(sh: Shape, kinds: str, names, tensors):
 
 def _invoke(entry: str, sh: Shape, kinds: str, names, tensors, stream):
     lens = getattr(sh, "_prefix_lens", None)
-    if lens is not None and sh.prefix_lens:
+    if lens is not None and sh.prefix_lens and isinstance(tensors[0], torch.Tensor):
         _call_device(sh, tensors[0])
     rc = _native().call(_address(entry), sh, kinds, tensors,
                         None if stream is None else stream.cuda_stream)

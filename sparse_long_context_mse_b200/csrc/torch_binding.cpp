@@ -89,46 +89,50 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     PyErr_SetString(PyExc_TypeError, "call: a losa_shape, and one tensor per kind");
     return nullptr;
   }
-  void* a[kMaxArgs + 2] = {};
-  int n = 0, dev = -1;
-  for (Py_ssize_t i = 0; i < nk; ++i) {
-    PyObject* o = PyTuple_GET_ITEM(args[3], i);
-    Want w;
-    if (!expect(kinds[i], sh, &w)) return PyLong_FromLong(-1);
-    if (o == Py_None && kinds[i] >= 'a' && kinds[i] <= 'z' && kinds[i] != 's' && kinds[i] != 'b') {
-      a[n++] = nullptr;
-      continue;
-    }
-    if (!THPVariable_Check(o)) return PyLong_FromLong(-1);
-    const at::Tensor& t = THPVariable_Unpack(o);
-    if (t.layout() != c10::kStrided || !t.is_cuda() || t.scalar_type() != w.type || !t.is_contiguous() ||
-        (dev >= 0 && t.get_device() != dev))
-      return PyLong_FromLong(-1);
-    dev = t.get_device();
-    if (w.nd >= 0) {
-      const auto sz = t.sizes();
-      if (static_cast<int>(sz.size()) != w.nd) return PyLong_FromLong(-1);
-      for (int j = 0; j < w.nd; ++j)
-        if (sz[j] != w.size[j]) return PyLong_FromLong(-1);
-    }
-    a[n++] = t.data_ptr();
-    if (kinds[i] == 'W') a[n++] = reinterpret_cast<void*>(t.numel());
+  void* stream = nullptr;
+  if (args[4] != Py_None) {
+    stream = PyLong_AsVoidPtr(args[4]);
+    if (PyErr_Occurred()) return nullptr;
   }
-  if (dev < 0) return PyLong_FromLong(-1);
-  int rc = 0;
-  try {
-    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    if (args[4] == Py_None) {
-      a[n] = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-    } else {
-      a[n] = PyLong_AsVoidPtr(args[4]);
-      if (PyErr_Occurred()) return nullptr;
+  void* a[kMaxArgs + 2] = {};
+  int n = 0, dev = -1, rc = 0;
+  try {  // (a tensor without strides or storage of its own throws when it is asked)
+    for (Py_ssize_t i = 0; i < nk; ++i) {
+      PyObject* o = PyTuple_GET_ITEM(args[3], i);
+      Want w;
+      if (!expect(kinds[i], sh, &w)) return PyLong_FromLong(-1);
+      if (o == Py_None && kinds[i] >= 'a' && kinds[i] <= 'z' && kinds[i] != 's' && kinds[i] != 'b') {
+        a[n++] = nullptr;
+        continue;
+      }
+      if (!THPVariable_Check(o)) return PyLong_FromLong(-1);
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (t.layout() != c10::kStrided || !t.is_cuda() || t.scalar_type() != w.type ||
+          !t.is_contiguous() || (dev >= 0 && t.get_device() != dev))
+        return PyLong_FromLong(-1);
+      dev = t.get_device();
+      if (w.nd >= 0) {
+        const auto sz = t.sizes();
+        if (static_cast<int>(sz.size()) != w.nd) return PyLong_FromLong(-1);
+        for (int j = 0; j < w.nd; ++j)
+          if (sz[j] != w.size[j]) return PyLong_FromLong(-1);
+      }
+      a[n++] = t.data_ptr();
+      if (kinds[i] == 'W') a[n++] = reinterpret_cast<void*>(t.numel());
     }
-    // (every parameter is a pointer or of a pointer's size; the entry point reads
-    // those that it has)
+    if (dev < 0) return PyLong_FromLong(-1);
+    c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+    a[n] = args[4] == Py_None
+               ? c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream()
+               : stream;
+    // A launch waits while the device's queue is full, perhaps for work of another
+    // Python thread: not under the interpreter's lock.  (Every parameter is a pointer
+    // or of a pointer's size; the entry point reads those that it has.)
+    PyThreadState* state = PyEval_SaveThread();
     rc = reinterpret_cast<Fn>(entry)(&sh, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9],
                                      a[10], a[11], a[12], a[13], a[14], a[15], a[16], a[17], a[18],
                                      a[19]);
+    PyEval_RestoreThread(state);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;

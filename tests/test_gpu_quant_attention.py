@@ -1,7 +1,9 @@
 """Attention over the 8-bit prefix cache: the dense pass against its 64-bit
-formula, the step against the step over the read-back prefix (the same kernels'
-arithmetic, so bit for bit) and against the oracle, and a whole block's life --
-write, dense pass, steps, append, next block."""
+formula, the step against the step over the read-back prefix (the same selections
+and weights), 64 bits and the oracle, and a whole block's life -- write, dense pass,
+steps, append, next block."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -285,6 +287,39 @@ def test_dense_calls_queued_behind_the_kernels_that_write_their_inputs(B):
         got.append({n: x.clone() for n, x in out.items()})
     for r, (_, c, _, qs, k, v) in zip(got, cases):
         check_dense(r, *dense_reference(sh, qs[0], *c, k, v))
+
+
+def test_dense_from_two_threads():
+    """Python threads, each with its own stream, tensors and workspace."""
+    cases = [inputs("bf16", [1500, 60], 2, 4, 16, seed=111), inputs("bf16", [900], 2, 8, 1, seed=112)]
+    got = [[], []]
+    torch.cuda.synchronize()
+
+    def work(i):
+        sh, cache, _, q, kb, vb = cases[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ws = api.alloc_workspace(sh, api.LOSA_WS_DENSE_QUANT, DEV)
+            for _ in range(50):
+                got[i].append(gpu_dense_quant(sh, q[0], cache, kb, vb, ws))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i, (sh, cache, _, q, kb, vb) in enumerate(cases):
+        assert len(got[i]) == 50
+        check_dense(got[i][0], *dense_reference(sh, q[0], *cache, kb, vb))
+        assert all(torch.equal(r[k], got[i][0][k]) for r in got[i] for k in r)
+
+
+def test_a_tensor_without_sizes_raises():
+    sh, cache, _, q, kb, vb = inputs("bf16", [40], 2, 2, 4, seed=3)
+    K, V = (torch.zeros(1, 2, 40, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    nested = torch.nested.nested_tensor([K[0], K[0]])
+    with pytest.raises((RuntimeError, ValueError)):
+        api.dequantize_prefix(sh, *cache, nested, V)
 
 
 # ---------------------------------------------------------------------------
