@@ -547,3 +547,59 @@ def test_two_blocks_of_a_generation(dtype, ragged):
         t += B
     assert api.read_device_status(ws_d) == api.read_device_status(ws_s) == api.LOSA_OK
     assert np.isfinite(f64(cache[0][:, :, :400])).all()
+
+
+def test_a_block_in_one_graph():
+    """Copies from host memory, the write on a side stream, the dense pass, two steps and the
+    append captured together and replayed on other inputs: the results of eager calls."""
+    S, Hkv, G, B, L = 2, 2, 4, 16, 900
+    sh = api.make_shape(S, Hkv * G, Hkv, 128, L, 16, B, 4, 64, "bf16", prefix_capacity=L + 40)
+    g = torch.Generator().manual_seed(77)
+    rnd = lambda *shape: torch.randn(*shape, generator=g).to(torch.bfloat16)
+    sets = [[rnd(S, Hkv, L + 40, 128), rnd(S, Hkv, L + 40, 128), rnd(3, S, Hkv * G, B, 128),
+             rnd(S, Hkv, B, 128), rnd(S, Hkv, B, 128)] for _ in range(2)]
+    ws_d = api.alloc_workspace(sh, api.LOSA_WS_DENSE_QUANT, DEV)
+    ws_s = api.alloc_workspace(sh, api.LOSA_WS_STEP, DEV)
+
+    def buffers():
+        return ([torch.empty_like(x, device=DEV) for x in sets[0]], api.alloc_quant_prefix(sh, DEV),
+                api.alloc_page_meta(sh, DEV).zero_(), alloc_state(sh, torch.device(DEV), 0.0))
+
+    def block(host, buf, side):
+        (K, V, q, kb, vb), cache, meta, st = buf
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for dst, src in zip((K, V), host):
+                dst.copy_(src, non_blocking=True)
+            api.quantize_prefix(sh, K, V, *cache, meta)
+        for dst, src in zip((q, kb, vb), host[2:]):
+            dst.copy_(src, non_blocking=True)
+        main.wait_stream(side)
+        tail = (st["o_p"], st["l_p"], st["out"], st["lse"])
+        api.dense_prefix_quant(sh, q[0], *cache, kb, vb, *tail, ws_d)
+        for i in (1, 2):
+            api.step_quant(sh, q[i], q[i - 1], *cache, meta, kb, vb, *tail, ws_s)
+        api.append_block_quant(sh, kb, vb, *cache, meta)
+        return [st[k] for k in ("o_p", "l_p", "out", "lse")] + [x.view(torch.uint8) for x in cache] + [meta]
+
+    host = [x.clone().pin_memory() for x in sets[0]]
+    buf, side = buffers(), torch.cuda.Stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        block(host, buffers(), side)  # (warm-up)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = block(host, buf, side)
+    for data in sets:
+        for dst, src in zip(host, data):
+            dst.copy_(src)
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        want = block([x.pin_memory() for x in data], buffers(), torch.cuda.Stream())
+        torch.cuda.synchronize()
+        assert torch.isfinite(want[2]).all()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
+    assert api.read_device_status(ws_d) == api.read_device_status(ws_s) == api.LOSA_OK
