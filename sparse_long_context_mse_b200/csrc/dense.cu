@@ -105,29 +105,37 @@ __device__ __forceinline__ void suffix_row(float4 q, const float* Kb, const floa
   L = (m + __log2f(l)) * kLn2;
 }
 
-constexpr int kFinishWarps = 4;   // rows (one per warp) per CTA of the dense finish
-constexpr int kFinishBatch = 18;  // splits' partials in flight per row (one round at 18 splits)
+constexpr int kFinishWarps = 4;   // rows per CTA of the dense finish
 
-__global__ void __launch_bounds__(kFinishWarps * 32)
+// PAIR: two warps per row, one for the attention over the block's own keys and one
+// for the partials, which it can load at once when the split kernel has ended (8-bit
+// prefix); else one warp does the one and then the other.  BATCH: partials in flight
+// per row.
+template <bool PAIR, int BATCH>
+__global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH <= 6 ? 3 : 0)
     dense_finish_kernel(const void* __restrict__ Q, const void* __restrict__ Kb,
                         const void* __restrict__ Vb, const float* __restrict__ part,
                         float* __restrict__ o_p, float* __restrict__ l_p, float* __restrict__ out,
                         float* __restrict__ out_lse, Dims d) {
   extern __shared__ __align__(16) float fsm[];  // the block's K then V, [Bpad][d] each
   __shared__ float Ps[kFinishWarps][kPS];
+  __shared__ float4 xo[PAIR ? kFinishWarps * 32 : 1];  // the row's (o_s, L_s) between its warps
+  __shared__ float xl[kFinishWarps];
   const int sh = blockIdx.x;  // s * Hq + h
   const int s = sh / d.Hq, h = sh % d.Hq, g = h / d.G;
   const int sg = s * d.Hkv + g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) % kFinishWarps, lane = threadIdx.x & 31;
+  const bool own = !PAIR || threadIdx.x >= kFinishWarps * 32;    // attends to the block
+  const bool merges = !PAIR || threadIdx.x < kFinishWarps * 32;  // merges the partials
   const int rows = d.G * d.B;
   const int Bpad = (d.B + kPS - 1) / kPS * kPS;
   float* Ksb = fsm;
   float* Vsb = fsm + Bpad * kD;
-  // one warp per row: row blockIdx.y * kFinishWarps + warp of head h
+  // row blockIdx.y * kFinishWarps + warp of head h
   const int t = blockIdx.y * kFinishWarps + warp;
   float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (t < d.B) q = ld4(Q, (static_cast<size_t>(sh) * d.B + t) * kD + 4 * lane, d.dtype);
-  for (int e = threadIdx.x; e < Bpad * kD / 4; e += blockDim.x) {
+  if (own && t < d.B) q = ld4(Q, (static_cast<size_t>(sh) * d.B + t) * kD + 4 * lane, d.dtype);
+  for (int e = threadIdx.x % (kFinishWarps * 32); own && e < Bpad * kD / 4; e += kFinishWarps * 32) {
     const int j = e / (kD / 4), c = (e % (kD / 4)) * 4;
     float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
     if (j < d.B) {
@@ -138,12 +146,13 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     *reinterpret_cast<float4*>(Ksb + j * kD + c) = kv;
     *reinterpret_cast<float4*>(Vsb + j * kD + c) = vv;
   }
-  __syncthreads();
+  if (!PAIR) __syncthreads();
+  else if (own) bar_sync(1, kFinishWarps * 32);
   // the group's partials: one per fixed split, or one per CTA whose range of
   // the line of tiles meets the group
   size_t first = static_cast<size_t>(sg) * d.nsplit;
   int nparts = d.nsplit;
-  if (d.line_ctas) {
+  if (merges && d.line_ctas) {
     long long before, all;
     line_sums(d, s, before, all);
     const long long total = all * d.Hkv;
@@ -156,26 +165,33 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
   // the row's attention over the block's own keys while the split kernel drains
   float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
   float Ls = 0.f;
-  if (t < d.B) suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
+  if (own && t < d.B) {
+    suffix_row(q, Ksb, Vsb, d.B, d.scale_log2, Ps[warp], os, Ls);
+    if (PAIR) {
+      xo[warp * 32 + lane] = os;
+      if (lane == 0) xl[warp] = Ls;
+      bar_sync(2 + warp, 64);
+    }
+  }
   // launched behind the split kernel (programmatic dependent launch): its
   // partials are read only after it has completed
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t < d.B) {
+  if (merges && t < d.B) {
     const size_t row = static_cast<size_t>(sh) * d.B + t;
     const int r = (h - g * d.G) * d.B + t;
     // merge the prefix partials (base-2 units) of every split in one pass,
-    // kFinishBatch splits' loads in flight at a time, the running sums rescaled when
+    // BATCH splits' loads in flight at a time, the running sums rescaled when
     // a batch raises the maximum
     const float* p0 = part + (first * rows + r) * kPartStride;
     const size_t pstride = static_cast<size_t>(rows) * kPartStride;
     float M = -INFINITY, lsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int s0 = 0; s0 < nparts; s0 += kFinishBatch) {
-      float mc[kFinishBatch], lc[kFinishBatch];
-      float4 ac[kFinishBatch];
+    for (int s0 = 0; s0 < nparts; s0 += BATCH) {
+      float mc[BATCH], lc[BATCH];
+      float4 ac[BATCH];
 #pragma unroll
-      for (int i = 0; i < kFinishBatch; ++i) {
+      for (int i = 0; i < BATCH; ++i) {
         mc[i] = -INFINITY;
         if (s0 + i < nparts) {
           const float* src = p0 + (s0 + i) * pstride;
@@ -186,7 +202,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
       }
       float Mh = M;
 #pragma unroll
-      for (int i = 0; i < kFinishBatch; ++i) Mh = fmaxf(Mh, mc[i]);
+      for (int i = 0; i < BATCH; ++i) Mh = fmaxf(Mh, mc[i]);
       const float rs = exp2f(M - Mh);  // 0 while nothing is accumulated
       lsum *= rs;
       acc.x *= rs;
@@ -194,7 +210,7 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
       acc.z *= rs;
       acc.w *= rs;
 #pragma unroll
-      for (int i = 0; i < kFinishBatch; ++i) {
+      for (int i = 0; i < BATCH; ++i) {
         if (s0 + i < nparts) {
           const float w = exp2f(mc[i] - Mh);
           lsum += w * lc[i];
@@ -211,6 +227,11 @@ __global__ void __launch_bounds__(kFinishWarps * 32)
     const float Lp = (M + __log2f(lsum)) * kLn2;
     *reinterpret_cast<float4*>(o_p + row * kD + 4 * lane) = op;
     if (lane == 0) l_p[row] = Lp;
+    if (PAIR) {
+      bar_sync(2 + warp, 64);
+      os = xo[warp * 32 + lane];
+      Ls = xl[warp];
+    }
     float4 o;
     float L;
     lse_merge(op, Lp, os, Ls, o, L);
@@ -659,9 +680,20 @@ int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const v
                         cudaStream_t st) {
   // behind the split kernel with programmatic dependent launch: the finish
   // CTAs stage the block's K/V while the split kernel drains
-  return launch_behind(dense_finish_kernel, dim3(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps),
-                       kFinishWarps * 32, 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float), st,
-                       q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
+  const dim3 grid(d.S * d.Hq, (d.B + kFinishWarps - 1) / kFinishWarps);
+  const size_t smem = 2u * ((d.B + kPS - 1) / kPS * kPS) * kD * sizeof(float);
+  const auto launch = [&](auto* fn, int warps) {
+    return launch_behind(fn, grid, 32 * warps, smem, st, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
+  };
+  if (!d.line_ctas) return launch(dense_finish_kernel<false, 18>, kFinishWarps);
+  // 8-bit prefix.  A KV head has about line_ctas / (S Hkv) partials per row: where
+  // they are many (few heads, so few CTAs here) one round of 18 loads per row ends
+  // first, else three small CTAs per SM.  A pass with single warps, with rounds of
+  // 18 and with rounds of 6: 8 KV heads, 64 rows, 64K prefix (19 partials) 43.1, 41.5
+  // and 43.2 us; 8K 16.8, 15.3 and 16.0; 8 x 32K, 128 rows (2 or 3) 289, 291 and 268;
+  // one token for 8 ragged sequences (3 or 4) 50.7, 54.5 and 50.3.
+  return d.line_ctas > 8 * d.S * d.Hkv ? launch(dense_finish_kernel<true, 18>, 2 * kFinishWarps)
+                                       : launch(dense_finish_kernel<true, 6>, 2 * kFinishWarps);
 }
 }  // namespace losa
 
