@@ -45,14 +45,16 @@
 //
 // Measured, calls back to back (with the finish kernel; the floor at the copy
 // bandwidth of 6.45 TB/s): 8 KV heads, 64K prefix, 134 MB, floor 21 us: 16 rows
-// per KV head 31.6 us, 32 rows 34.0, 64 rows 43.1.  Up to 32 rows it is bound by
+// per KV head 31.7 us, 32 rows 33.0, 64 rows 42.0.  Up to 32 rows it is bound by
 // the loads (what is left of it with the softmax taken out takes 28 us: 23 for
 // the bytes, and a prologue and an end that no tile overlaps).  With 64 rows a
 // tile's 2000 cycles go to the softmax warps: 8192 weights, each scaled, voted
 // on, raised to a power of two and split in two fp16 numbers, some 5200 warp
 // instructions at 0.65 a cycle and scheduler, with no pipe above 40 % busy and
-// the tensor core at 40 %.  Eight sequences of 32K and 128 rows (two CTAs each
-// range), floor 85 us: 285 us, the same softmax.
+// the tensor core at 33 %.  Eight sequences of 32K and 128 rows (two CTAs each
+// range), floor 85 us: 267 us, the same softmax.  In loops of more than a few
+// milliseconds the 64-row passes draw the card's 1000 W and the clock falls from
+// 1.92 to 1.65 GHz: 48 and 316 us.
 #include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
