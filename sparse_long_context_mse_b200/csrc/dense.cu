@@ -11,6 +11,7 @@
 // CUDA cores.
 #include <mutex>
 
+#include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
@@ -224,7 +225,14 @@ __global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH
     }
     const float inv = 1.f / lsum;
     const float4 op = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    const float Lp = (M + __log2f(lsum)) * kLn2;
+    float Lp = (M + __log2f(lsum)) * kLn2;
+    if (PAIR) {
+      // (an 8-bit pass's reference puts the row's maximum at 2^11 or so, and divides its
+      // sum by the V scales: the whole numbers of the two logarithms are added first)
+      const int e = static_cast<int>(__float_as_uint(lsum) >> 23) - 127;
+      if (e > -127 && e < 127 && fabsf(M) < 1048576.f)
+        Lp = (M + static_cast<float>(e) + __log2f(lsum * exp2_int(-e))) * kLn2;
+    }
     *reinterpret_cast<float4*>(o_p + row * kD + 4 * lane) = op;
     if (lane == 0) l_p[row] = Lp;
     if (PAIR) {
