@@ -27,11 +27,16 @@
 //   smaller range: 2^-17, and twice the results' error).  fp32 takes six e4m3
 //   parts, the last three 2^12 times larger in an accumulator of their own, within
 //   2^-29 of the row's maximum.
-// * O^T = V8^T W: W in fp16 (its rounding, and the rounding's remainder as a
-//   second fp16 operand: 22 bits), so V8 has to be fp16 too.  Four warps
-//   transpose V codes out of shared memory (ldmatrix, bytes), widen them (exact)
-//   and store them as the A operand in TMEM, which costs 1/8 of the shared-memory
-//   traffic of an fp16 tile there; W goes through shared memory as the MN-major B.
+// * O^T = V8^T W: W as the sum of three bf16 numbers, its top, middle and low 8
+//   bits: all 24 of an fp32 number, at any size an fp32 number can have.  What holds
+//   a row's weight need not be what its output is made of (a page or a token of
+//   zeros, values far smaller than another page's), so a weight keeps its own
+//   relative accuracy, however far it lies below the reference.  (Two fp16 parts
+//   are cheaper -- 64 rows, 64K prefix 49.2 us in place of 53.3 -- and have 22 bits,
+//   but only of weights within 2^-13 of the largest; below 2^-36 they are zero.)  V8 has to be bf16 too.  Four warps transpose V codes out of
+//   shared memory (ldmatrix, bytes), widen them (exact) and store them as the A
+//   operand in TMEM, which costs 1/8 of the shared-memory traffic of a 16-bit tile
+//   there; W goes through shared memory as the MN-major B.
 // * A softmax thread owns one key (TMEM lane) and 8 or 16 of the query columns:
 //   the page scales are constants of the thread, l is a sum in registers across tiles
 //   (joined over the lanes at the end), and no tile needs a maximum over the
@@ -67,7 +72,7 @@ namespace {
 // V, then one that loads, one that issues MMAs, one that prepares the tiles'
 // scales and one that has nothing to do.
 constexpr int kTileBytes = kLineKeys * kD;  // one K or V tile of codes: 16 KB
-constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (fp16 pairs)
+constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (bf16 pairs)
 constexpr float kRefTop = 11.f;             // a new reference puts the row's maximum at 2^11 ..
 constexpr float kRefMove = 15.f;            // .. and stays until a weight would pass 2^15
 constexpr float kPartScale = 4096.f;        // fp32: parts 4-6 are this much larger
@@ -118,8 +123,8 @@ struct QPlan {
   static_assert(soft * soft_regs + 256 * other_regs <= threads * regs, "register split");
   static constexpr int cw = NR / nwg;                    // columns per softmax warp group
   static constexpr int na = NQ > 3 ? 2 : 1;              // score accumulators
-  static constexpr int atom = kLineKeys * 128;           // 64 fp16 columns of W: 16 KB
-  static constexpr int wbytes = 2 * atom;                // W and its remainder
+  static constexpr int atom = kLineKeys * 128;           // 64 bf16 columns of W: 16 KB
+  static constexpr int wbytes = 3 * atom;                // the three parts of W
   static constexpr int qbytes = NQ * NR * kD;
   static constexpr int small = 3 * 1024;                    // barriers, row factors, exchange
   static constexpr int room = kB200MaxDynSmem - small - qbytes - 2 * wbytes;
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
     return;
   }
   char* qs = sm;                              // NQ parts of [NR][128 B]
-  char* wbuf = qs + C::qbytes;                // [2] W buffers: [2 (W, remainder)][128][128 B]
+  char* wbuf = qs + C::qbytes;                // [2] W buffers: [3 (parts)][128][128 B]
   char* kring = wbuf + 2 * C::wbytes;         // ST K tiles
   char* vring = kring + ST * kTileBytes;      // ST V tiles
   uint64_t* bars = reinterpret_cast<uint64_t*>(vring + ST * kTileBytes);
@@ -299,8 +304,8 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       // ---- MMAs: the whole warp follows the loop, one elected thread issues
       constexpr uint32_t idS = umma_idesc_e4m3(128, NR);
       constexpr uint32_t idS2 = umma_idesc_e4m3(128, NR, NQ == 2);
-      constexpr uint32_t idO = umma_idesc_f16_bmn(128, NR);
-      constexpr uint32_t idR = idO | (1u << 14);  // minus B: the remainder is stored negated
+      constexpr uint32_t idO = umma_idesc_bf16(128, NR, 1);
+      constexpr uint32_t idM = idO | (1u << 14);  // minus B: the middle part is stored negated
       const uint64_t dq = umma_desc(su32(qs), 16, 1024), dk = umma_desc(su32(kring), 16, 1024);
       const uint64_t dw = umma_desc(su32(wbuf), C::atom, 1024);
       const uint32_t q_lo = desc_lo(dq), k_lo = desc_lo(dk), kq_hi = desc_hi(dq);
@@ -355,14 +360,14 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
         const uint32_t to = tb + C::tO + par * NR, tv = tb + C::tV + par * kVCols;
         const uint32_t me = elect_one();
 #pragma unroll
-        for (int h = 1; h >= 0; --h)  // (the remainder first)
+        for (int h = 2; h >= 0; --h)  // (the small parts first)
 #pragma unroll
           for (int k = 0; k < kLineKeys / 16; ++k) {
             const uint32_t b = wl + ((h * C::atom + k * 16 * 128) >> 4);
-            if (h == 1 && k == 0)
-              umma_f16_ta<false>(me, to, tv + k * 8, b, w_hi, idR);
+            if (h == 2 && k == 0)
+              umma_f16_ta<false>(me, to, tv + k * 8, b, w_hi, idO);
             else
-              umma_f16_ta<true>(me, to, tv + k * 8, b, w_hi, h == 1 ? idR : idO);
+              umma_f16_ta<true>(me, to, tv + k * 8, b, w_hi, h == 1 ? idM : idO);
           }
         umma_commit_if(me, &bO[par]);
         if (more && fresh) issue_s(par ^ 1, true);
@@ -396,7 +401,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
         if (lane == 0) mbar_arrive(&bS[it & 1]);
       }
     } else if (warp < W0 + 4) {
-      // ---- V codes -> fp16, transposed, into TMEM: warp w4 has the channels
+      // ---- V codes -> bf16, transposed, into TMEM: warp w4 has the channels
       // 32 w4 .. (its TMEM lanes)
       const int w4 = warp & 3;
       const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           for (int kq = 0; kq < 2; ++kq) {
             uint32_t f[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e4m3x4_to_f16x2(c[kq * 8 + i], f[2 * i], f[2 * i + 1]);
+            for (int i = 0; i < 8; ++i) e4m3x4_to_bf16x2(c[kq * 8 + i], f[2 * i], f[2 * i + 1]);
             tmem_st16x256_x4_raw(tb + C::tV + (it & 1) * kVCols + kq * 32 + lane_off +
                                      (static_cast<uint32_t>(dh * 16) << 16),
                                  f);
@@ -626,21 +631,23 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       char* wrow = wbuf + (it & 1) * C::wbytes + key * 128;
 #pragma unroll
       for (int i = 0; i < CW; i += 8) {
-        uint32_t hi[4], lo[4];
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 a = up(y[i / 2 + u]);
-          const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-          const u64 w2 = pk(w.x, w.y);
-          l[i / 2 + u] = fma2(w2, rv2, l[i / 2 + u]);
-          hi[u] = pack_f16x2(w.x, w.y);
-          const float2 r = f16x2_sub(hi[u], w);  // minus the remainder
-          lo[u] = pack_f16x2(r.x, r.y);
+          const u64 w = pk(ex2_approx(a.x), ex2_approx(a.y));
+          l[i / 2 + u] = fma2(w, rv2, l[i / 2 + u]);
+          // cut off, not rounded: what a part leaves is exact; mid is stored negated
+          hi[u] = bf16x2_top(up(w));
+          const float2 r = bf16x2_sub(hi[u], up(w));
+          mid[u] = bf16x2_top(r);
+          lo[u] = bf16x2_top(bf16x2_sub(mid[u], r));
         }
         // the 16-byte chunk of these columns in the key's row
         char* dst = wrow + ((((c0 + i) >> 3) ^ (key & 7)) << 4);
         *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + C::atom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(dst + C::atom) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+        *reinterpret_cast<uint4*>(dst + 2 * C::atom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_async_smem();
       tc_fence_before();

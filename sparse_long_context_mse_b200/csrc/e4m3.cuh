@@ -44,6 +44,15 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
       : "r"(h));
   return r;
 }
+// Four codes -> bf16 pairs (codes 0, 1) and (codes 2, 3), exact (an e4m3 number has
+// 4 significant bits, so the upper halves of the fp32 numbers hold all of it).
+__device__ __forceinline__ void e4m3x4_to_bf16x2(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  e4m3x4_to_f16x2(c, a, b);
+  const float2 x = f16x2_to_f32(a), y = f16x2_to_f32(b);
+  lo = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+  hi = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+}
 __device__ __forceinline__ uint32_t f16x2_min(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

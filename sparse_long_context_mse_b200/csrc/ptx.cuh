@@ -175,20 +175,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// (the fp16 numbers of h) - x, exact where the difference is an fp32 number.
-__device__ __forceinline__ float2 f16x2_sub(uint32_t h, float2 x) {
+// (the bf16 numbers of h) - x, exact where the difference is an fp32 number.
+__device__ __forceinline__ float2 bf16x2_sub(uint32_t h, float2 x) {
   float2 r;
-  asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n sub.f32.f16 %0, l, %3;\n"
-      " sub.f32.f16 %1, h, %4;\n}"
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n sub.f32.bf16 %0, l, %3;\n"
+      " sub.f32.bf16 %1, h, %4;\n}"
       : "=f"(r.x), "=f"(r.y)
       : "r"(h), "f"(x.x), "f"(x.y));
   return r;
 }
-// Two fp32 values -> packed fp16x2 (round to nearest even), low half first.
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+// Two fp32 values -> packed bf16x2, cut off (their upper halves), low half first.
+__device__ __forceinline__ uint32_t bf16x2_top(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
 }
 // Two fp32 values -> packed bf16x2 (round to nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

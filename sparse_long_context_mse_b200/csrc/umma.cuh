@@ -149,12 +149,6 @@ __device__ __forceinline__ void tmem_st16x256_x4(uint32_t taddr, const float (&v
 __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N, bool b_e5m2 = false) {
   return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B, A K-major
-// (in TMEM: lane = row, a 32-bit column holds two consecutive k), B MN-major.
-__host__ __device__ constexpr uint32_t umma_idesc_f16_bmn(int M, int N) {
-  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
 // The forms below are issued by a whole warp in uniform control flow; the
 // thread whose `me` is set executes them (elect_one: so that descriptors and
 // TMEM addresses stay in uniform registers, and an MMA costs a few
@@ -180,7 +174,8 @@ __device__ __forceinline__ void umma_e4m3(uint32_t me, uint32_t d_tmem, uint32_t
       "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] . B[smem], 16-bit operands.
+// D[tmem] (+)= A[tmem] . B[smem], 16-bit operands (A in TMEM: lane = row, a 32-bit
+// column holds two consecutive k).
 template <bool ACC>
 __device__ __forceinline__ void umma_f16_ta(uint32_t me, uint32_t d_tmem, uint32_t a_tmem,
                                             uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {

@@ -1,0 +1,103 @@
+"""The dense pass over the 8-bit prefix where the pages' V scales and the keys' weights are of
+very different sizes: what holds the weight need not be what the output is made of.
+
+Errors are relative to the results' norm, so that small values count as much as large ones."""
+import math
+
+import pytest
+import torch
+
+from losa_testutil import DEV
+from quant_testutil import dense_reference, gpu_dense_quant
+from sparse_long_context_mse_b200 import api
+from test_gpu_quant_attention import inputs
+
+pytestmark = pytest.mark.gpu
+
+PS = 16
+
+
+def run(sh, cache, q, kb, vb):
+    ws = api.alloc_workspace(sh, api.LOSA_WS_DENSE_QUANT, DEV)
+    got = gpu_dense_quant(sh, q, cache, kb, vb, ws)
+    assert api.read_device_status(ws) == api.LOSA_OK
+    return got, dense_reference(sh, q, *cache, kb, vb)[0]
+
+
+def errors(got, ref):
+    """(worst relative error of o_p and out by norm, worst error of the log-normalisers)."""
+    rel = [((got[k].cpu().double() - ref[k]).norm() / ref[k].norm()).item() for k in ("o_p", "out")]
+    return max(rel), max((got[k].cpu().double() - ref[k]).abs().max().item() for k in ("l_p", "lse"))
+
+
+# one row to 128, few tiles and many for each CTA, ragged, both types
+SHAPES = [("bf16", [700], 2, 4, 16), ("bf16", [20000], 8, 4, 1), ("bf16", [9000, 501], 2, 4, 32),
+          ("bf16", [1000], 1, 8, 4), ("f32", [3000], 2, 4, 4), ("f32", [700, 90], 1, 8, 16)]
+
+
+@pytest.mark.parametrize("amp", [1e-2, 1e-4, 1e-9])
+@pytest.mark.parametrize("dtype,lens,Hkv,G,B", SHAPES)
+def test_small_values_beside_pages_of_zeros(dtype, lens, Hkv, G, B, amp):
+    """A page of zeros has scale 1, whatever its neighbours have, and a share of the weight.
+    The pass's roundings are relative to each key's own weight, so the bound is that of values
+    of one size (test_dense_error_against_64_bits): 2^-20 of the norm."""
+    sh, cache, _, q, kb, vb = inputs(dtype, lens, Hkv, G, B, seed=sum(lens) + 7)
+    g = torch.Generator().manual_seed(5)
+    K, V = (torch.randn(len(lens), Hkv, sh.capacity, 128, generator=g) for _ in range(2))
+    V *= amp
+    for p in range(3, sh.capacity_pages, 7):
+        V[:, :, p * PS:(p + 1) * PS] = 0.0
+    api.quantize_prefix(sh, K.to(sh.torch_dtype).to(DEV), V.to(sh.torch_dtype).to(DEV), *cache)
+    assert (cache[3][:, :, 3] == 1.0).all()
+    got, ref = run(sh, cache, q[0], kb, (vb.float() * amp).to(sh.torch_dtype))
+    o, l = errors(got, ref)
+    assert o <= 2.0 ** -20, o
+    assert l <= 2.0 ** -19, l  # (a weight's relative error, and 2^-23 of its size, at most 10)
+
+
+@pytest.mark.parametrize("binades", [12, 30, 60])
+@pytest.mark.parametrize("dtype,lens,Hkv,G,B", SHAPES)
+def test_zero_values_hold_the_weight(dtype, lens, Hkv, G, B, binades):
+    """One token in 64 has a V of zeros and a score `binades` powers of two above the others:
+    the output is the others' part.  Their scores have no large term, so among themselves they
+    keep 2^-20; the normaliser is the heavy tokens' and carries their scores' error: t = 0.7 *
+    binades + 3 (natural-log units), summed in 8 accumulations of at most 2^-24 t (16 in fp32,
+    whose parts end in two accumulators) and rounded by half of 2^-23 t four times."""
+    sh, cache, _, q, kb, vb = inputs(dtype, lens, Hkv, G, B, seed=sum(lens) + 11)
+    g = torch.Generator().manual_seed(6)
+    K, V = (torch.randn(len(lens), Hkv, sh.capacity, 128, generator=g) for _ in range(2))
+    K[..., 0] = 0.0
+    heavy = torch.arange(5, sh.capacity, 64)
+    K[:, :, heavy, 0] = binades * math.log(2) / (8 * 128 ** -0.5)
+    V[:, :, heavy] = 0.0
+    api.quantize_prefix(sh, K.to(sh.torch_dtype).to(DEV), V.to(sh.torch_dtype).to(DEV), *cache)
+    q[0][..., 0] = 8.0
+    # (the block's tokens score like the light ones; its values are far smaller than the output)
+    kb[..., 0] = 0.0
+    got, ref = run(sh, cache, q[0], kb, torch.zeros_like(vb))
+    o, l = errors(got, ref)
+    t = 0.7 * binades + 3
+    tol = 2.0 ** -20 + t * (16 + 4) * 2.0 ** -24
+    assert ref["o_p"].norm() > 0 and o <= tol, (o, tol)
+    assert l <= tol + 2.0 ** -22 * ref["lse"].abs().max().item(), l
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scales_and_scores_against_each_other(dtype):
+    """Pages of values 2^20 and of values 2^-20 whose scores make up for it, and the same with
+    2^40 more between the two: the larger values' part is what the output is made of, or the
+    smaller values' is."""
+    sh, cache, _, q, kb, vb = inputs(dtype, [5000], 2, 4, 8, seed=71)
+    for up, down in ((40, 0), (80, 0), (0, 0)):  # score of the small values' pages, binades
+        g = torch.Generator().manual_seed(8)
+        K, V = (torch.randn(1, 2, sh.capacity, 128, generator=g) for _ in range(2))
+        K[..., 0] = 0.0
+        for p in range(sh.capacity_pages):
+            t = slice(p * PS, (p + 1) * PS)
+            V[:, :, t] *= 2.0 ** (20 if p % 5 else -20)
+            K[:, :, t, 0] = (down if p % 5 else up) * math.log(2) / (8 * 128 ** -0.5)
+        api.quantize_prefix(sh, K.to(sh.torch_dtype).to(DEV), V.to(sh.torch_dtype).to(DEV), *cache)
+        q[0][..., 0] = 8.0
+        got, ref = run(sh, cache, q[0], kb, torch.zeros_like(vb))
+        t = 0.7 * up + 3  # (as above)
+        assert errors(got, ref)[0] <= 2.0 ** -20 + t * 20 * 2.0 ** -24
