@@ -290,9 +290,9 @@ int losa_step_ref(const losa_shape* shape, const void* q_cur, void* q_ref,
  * holds, code * scale, so that the bound stays a bound of what is attended to.
  *
  * The calls that read a cache take any finite scales, also ones written by
- * another program, of which the V scales are >= 0 (the attention calls take a V
- * scale below 2^-100 as 2^-100; the dense pass is accurate while the V scales
- * of a KV head lie within 2^100 of each other).  Scales and codes of pages and
+ * another program, of which the V scales are >= 0 (zeros among them).  The
+ * attention calls are accurate for V scales of 2^-100 and more, the dense pass
+ * while those of a KV head lie within 2^100 of each other.  Scales and codes of pages and
  * tokens past a sequence's length are never used, whatever they hold, and never
  * written.
  * Scale arrays need the alignment of a float only (a layer's slice of a larger

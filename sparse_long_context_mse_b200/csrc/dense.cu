@@ -109,9 +109,9 @@ __device__ __forceinline__ void suffix_row(float4 q, const float* Kb, const floa
 constexpr int kFinishWarps = 4;   // rows per CTA of the dense finish
 
 // PAIR: two warps per row, one for the attention over the block's own keys and one
-// for the partials, which it can load at once when the split kernel has ended (8-bit
-// prefix); else one warp does the one and then the other.  BATCH: partials in flight
-// per row.
+// for the partials, which it can load at once when the split kernel has ended, and
+// partial sums in units of 2^E, E beside the maximum and the normaliser (8-bit prefix);
+// else one warp does the one and then the other.  BATCH: partials in flight per row.
 template <bool PAIR, int BATCH>
 __global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH <= 6 ? 3 : 0)
     dense_finish_kernel(const void* __restrict__ Q, const void* __restrict__ Kb,
@@ -185,50 +185,65 @@ __global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH
     // a batch raises the maximum
     const float* p0 = part + (first * rows + r) * kPartStride;
     const size_t pstride = static_cast<size_t>(rows) * kPartStride;
-    float M = -INFINITY, lsum = 0.f;
+    float M = -INFINITY, lsum = 0.f, E = -126.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int s0 = 0; s0 < nparts; s0 += BATCH) {
-      float mc[BATCH], lc[BATCH];
+      float mc[BATCH], lc[BATCH], ec[BATCH];
       float4 ac[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
         mc[i] = -INFINITY;
         if (s0 + i < nparts) {
           const float* src = p0 + (s0 + i) * pstride;
-          mc[i] = __ldcg(src);
-          lc[i] = __ldcg(src + 1);
+          if (PAIR) {
+            const float4 hd = __ldcg(reinterpret_cast<const float4*>(src));
+            mc[i] = hd.x;
+            lc[i] = hd.y;
+            ec[i] = hd.z;
+          } else {
+            mc[i] = __ldcg(src);
+            lc[i] = __ldcg(src + 1);
+          }
           ac[i] = __ldcg(reinterpret_cast<const float4*>(src + 4) + lane);
         }
       }
-      float Mh = M;
+      float Mh = M, Eh = E;
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) Mh = fmaxf(Mh, mc[i]);
+      for (int i = 0; i < BATCH; ++i) {
+        Mh = fmaxf(Mh, mc[i]);
+        if (PAIR && s0 + i < nparts) Eh = fmaxf(Eh, ec[i]);
+      }
       const float rs = exp2f(M - Mh);  // 0 while nothing is accumulated
+      const float ra = PAIR ? rs * exp2f(E - Eh) : rs;
       lsum *= rs;
-      acc.x *= rs;
-      acc.y *= rs;
-      acc.z *= rs;
-      acc.w *= rs;
+      acc.x *= ra;
+      acc.y *= ra;
+      acc.z *= ra;
+      acc.w *= ra;
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
         if (s0 + i < nparts) {
           const float w = exp2f(mc[i] - Mh);
+          const float wa = PAIR ? w * exp2f(ec[i] - Eh) : w;
           lsum += w * lc[i];
-          acc.x += w * ac[i].x;
-          acc.y += w * ac[i].y;
-          acc.z += w * ac[i].z;
-          acc.w += w * ac[i].w;
+          acc.x += wa * ac[i].x;
+          acc.y += wa * ac[i].y;
+          acc.z += wa * ac[i].z;
+          acc.w += wa * ac[i].w;
         }
       }
       M = Mh;
+      E = Eh;
     }
     const float inv = 1.f / lsum;
-    const float4 op = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    float4 op = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     float Lp = (M + __log2f(lsum)) * kLn2;
     if (PAIR) {
-      // (an 8-bit pass's reference puts the row's maximum at 2^11 or so, and divides its
-      // sum by the V scales: the whole numbers of the two logarithms are added first)
+      const float unit = exp2_int(static_cast<int>(E));
+      op = make_float4(op.x * unit, op.y * unit, op.z * unit, op.w * unit);
+      // (an 8-bit pass's reference may lie below the row's maximum: the whole numbers of
+      // the two logarithms are added first)
       const int e = static_cast<int>(__float_as_uint(lsum) >> 23) - 127;
       if (e > -127 && e < 127 && fabsf(M) < 1048576.f)
         Lp = (M + static_cast<float>(e) + __log2f(lsum * exp2_int(-e))) * kLn2;

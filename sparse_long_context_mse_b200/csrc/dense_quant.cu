@@ -1,15 +1,15 @@
 // dense_quant.cu -- the dense pass over a prefix cache held in 8 bits.
 //
-// s_j = scale * ks(page j) * (q . k8_j);  o = sum_j e^(s_j - m) vs(page j) v8_j
-// / sum_j e^(s_j - m): the page scales are factors of a key's score and of its
-// value.  In base 2, with x_j = s_j log2(e) + log2 vs_j and a reference m' per
-// row, the kernel accumulates
+// The page scales are factors of a key's score and of its value.  In base 2, with
+// x_j = scale * ks(page j) * (q . k8_j) * log2(e), a reference m per row and a power
+// of two 2^E near the largest V scale, the kernel accumulates
 //
-//   w_j = 2^(x_j - m'),   O = sum_j w_j v8_j,   l = sum_j w_j / vs_j,   o = O / l,
+//   p_j = 2^(x_j - m),   l = sum_j p_j,   W_j = p_j vs(page j) 2^-E,
+//   O = sum_j W_j v8_j,   o = 2^E O / l,
 //
-// so that one reference bounds what is accumulated, however different the V
-// scales of the pages are: a page of small values that holds the weight keeps
-// its relative accuracy.
+// E is that of the first tile of a KV head's keys and moves, as a reference does, when
+// a tile's largest scale passes 2^(E + 32): nothing overflows or loses bits while the
+// V scales of a head's keys lie within 2^100 of each other, whatever their size.
 //
 // Its floor is HBM: 256 bytes per key and KV head, read once.  The work is laid
 // out so that little on the chip takes longer:
@@ -73,8 +73,10 @@ namespace {
 // scales and one that has nothing to do.
 constexpr int kTileBytes = kLineKeys * kD;  // one K or V tile of codes: 16 KB
 constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (bf16 pairs)
-constexpr float kRefTop = 11.f;             // a new reference puts the row's maximum at 2^11 ..
-constexpr float kRefMove = 15.f;            // .. and stays until a weight would pass 2^15
+// A row's reference is its largest score when it is set, and stays until a weight would
+// pass 2^4; E likewise.  So O stays below 2^(4 + 33 + 9) per key.
+constexpr float kRefMove = 4.f;
+constexpr int kScaleMove = 32;
 constexpr float kPartScale = 4096.f;        // fp32: parts 4-6 are this much larger
 
 typedef unsigned long long u64;
@@ -140,8 +142,8 @@ struct QPlan {
 
 // What the softmax warps have to know of a tile.
 struct __align__(16) TileInfo {
-  // a page's score factor, log2 and reciprocal of the value scale; and, in every
-  // entry, the tile's real keys, + 256 if it is the KV head's last in this CTA
+  // a page's score factor and its value scale times 2^-E; and, in every entry, E and
+  // the tile's real keys, + 256 if it is the KV head's last in this CTA
   float4 page[kLineKeys / kPS];
 };
 
@@ -374,10 +376,11 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       }
     } else if (warp == W0 + 6 && n > 0) {
       // ---- a tile's scales: lane p < 8 its page p's, read a tile ahead
-      float k_ = 1.f, v_ = 1.f;
+      float k_ = 1.f, v_ = 0.f;
       auto fetch = [&]() {
         const int j = pos.lt * kLineKeys + lane * kPS;
-        k_ = v_ = 1.f;
+        k_ = 1.f;
+        v_ = 0.f;
         if (lane < kLineKeys / kPS && j < pos.L) {
           const size_t i = static_cast<size_t>(pos.s * d.Hkv + pos.g) * d.Pc + (j >> 4);
           k_ = __ldg(ks + i);
@@ -385,13 +388,17 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
         }
       };
       fetch();
+      int E = 0;
 #pragma unroll 1
       for (int it = 0; it < n; ++it) {
         const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
-        const float v = fmaxf(v_, kMinScale);
+        // (non-negative floats are ordered like their bits)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v_, 0.f)));
+        const int e = min(max(static_cast<int>(top >> 23) - 127, -126), 126);
+        if (it == 0 || pos.lt == 0 || e > E + kScaleMove) E = e;
         pos.next(d);
         const bool last = it + 1 == n || pos.lt == 0;
-        const float4 w = make_float4(k_ * d.scale_log2, log2f(v), 1.f / v,
+        const float4 w = make_float4(k_ * d.scale_log2, v_ * exp2_int(-E), __int_as_float(E),
                                      __int_as_float(nv + (last ? 256 : 0)));
         if (it + 1 < n) fetch();
         // (the info of two tiles back has been read)
@@ -462,6 +469,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
     float* ag = alpha + wg * CW;
     u64 l[CW / 2], o[CW / 2];
     bool fresh = true;
+    int E = 0;  // of what o holds
     bool pend1 = false, pend2 = false;  // O of one / two tiles back is still to be read
 
     // o += O buffer b (one tile's product)
@@ -476,11 +484,13 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       tmem_ld_wait(t);
       add_o(t);
     };
-    // the scores as exponents of 2, without the reference: S rf kf + lv
     auto s_addr = [&](int it, int a) {
       return tb + C::tS + (it & 1) * (NA * NR) + a * NR + c0 + lane_off;
     };
-    auto to_x = [&](int it, u64 kf2, u64 lv2, const float (&a)[CW], u64 (&y)[CW / 2]) {
+    // the scores as exponents of 2: S rf kf, less the reference in one rounding (ref:
+    // a score that makes a new reference and the weights of its tile are the rounded
+    // product instead, so that the largest weight is 1 however large the scores are)
+    auto to_x = [&](int it, u64 kf2, bool ref, const float (&a)[CW], u64 (&y)[CW / 2]) {
 #pragma unroll
       for (int i = 0; i < CW; i += 2) y[i / 2] = pk(a[i], a[i + 1]);
       if (NA == 2) {
@@ -494,8 +504,15 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
 #pragma unroll
       for (int i = 0; i < CW; i += 4) {
         const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(rf + c0 + i);
-        y[i / 2] = fma2(mul2(y[i / 2], r.x), kf2, lv2);
-        y[i / 2 + 1] = fma2(mul2(y[i / 2 + 1], r.y), kf2, lv2);
+        const u64 f0 = mul2(r.x, kf2), f1 = mul2(r.y, kf2);
+        if (ref) {
+          y[i / 2] = mul2(y[i / 2], f0);
+          y[i / 2 + 1] = mul2(y[i / 2 + 1], f1);
+        } else {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + c0 + i);
+          y[i / 2] = fma2(y[i / 2], f0, m.x);
+          y[i / 2 + 1] = fma2(y[i / 2 + 1], f1, m.y);
+        }
       }
     };
 #pragma unroll 1
@@ -504,6 +521,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
         // ---- a KV head begins: its queries, in parts (the S MMAs that read
         // the previous head's are done: this thread has waited for them)
         pend1 = pend2 = false;
+        E = 1024;  // (none yet: the first tile's takes its place)
 #pragma unroll
         for (int i = 0; i < CW / 2; ++i) l[i] = o[i] = 0ull;
         const size_t q0 = ((static_cast<size_t>(pos.s) * d.Hq + pos.g * d.G) * d.B + r0) * kD;
@@ -558,30 +576,26 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
       const int nv = __float_as_int(pg.w) & 255;
       const bool last = __float_as_int(pg.w) >= 256;
       const bool valid = key < nv;
-      const u64 kf2 = pk(pg.x, pg.x), lv2 = pk(pg.y, pg.y);
-      const float rv = valid ? pg.z : 0.f;
-      const u64 rv2 = pk(rv, rv);
+      const int new_e = __float_as_int(pg.z);
+      const u64 kf2 = pk(pg.x, pg.x), vs2 = pk(pg.y, pg.y);
       if (pend2) take_o(it & 1);
       tmem_ld_wait(sc);
       u64 y[CW / 2];
-      to_x(it, kf2, lv2, sc, y);
+      to_x(it, kf2, false, sc, y);
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < CW; i += 4) {
-        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + c0 + i);
-        y[i / 2] = add2(y[i / 2], m.x);
-        y[i / 2 + 1] = add2(y[i / 2 + 1], m.y);
         const float2 a = up(y[i / 2]), b = up(y[i / 2 + 1]);
         top = max3(max3(top, a.x, a.y), b.x, b.y);
       }
       pend2 = pend1;
-      if (bar_or(1 + wg, 128, valid && top > kRefMove)) {
-        // ---- some row's reference moves (the first tile; then seldom): the
+      if (bar_or(1 + wg, 128, (valid && top > kRefMove) || new_e != E)) {
+        // ---- some row's reference or E moves (the first tile; then seldom): the
         // columns' maxima over the tile's keys, references, and what has been
         // accumulated against the old ones
         tmem_ld_async(s_addr(it, 0), sc);
         tmem_ld_wait(sc);
-        to_x(it, kf2, lv2, sc, y);
+        to_x(it, kf2, true, sc, y);
         float mine = -INFINITY;
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
@@ -599,8 +613,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           for (int w = 1; w < 4; ++w) m = fmaxf(m, xg[w * CW + lane]);
           const float old = -nm[c0 + lane];
           const bool move = m > old + kRefMove || (old == -INFINITY && m > old);
-          // (exponents so large that 11 is lost in their rounding: m itself)
-          const float ref = !move ? old : fabsf(m) < 1048576.f ? m - kRefTop : m;
+          const float ref = move ? m : old;
           ag[lane] = move ? exp2f(old - ref) : 1.f;
           nm[c0 + lane] = -ref;
         }
@@ -612,10 +625,13 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           take_o((it - 1) & 1);
           pend2 = false;
         }
+        const float f = exp2_int(max(min(E - new_e, 0), -126));
+        const u64 f2 = pk(f, f);
+        E = new_e;
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
           const u64 a = *reinterpret_cast<const u64*>(ag + i);
-          o[i / 2] = mul2(o[i / 2], a);
+          o[i / 2] = mul2(mul2(o[i / 2], a), f2);
           l[i / 2] = mul2(l[i / 2], a);
           y[i / 2] = add2(y[i / 2], *reinterpret_cast<const u64*>(nm + c0 + i));
         }
@@ -635,11 +651,12 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const float2 a = up(y[i / 2 + u]);
-          const u64 w = pk(ex2_approx(a.x), ex2_approx(a.y));
-          l[i / 2 + u] = fma2(w, rv2, l[i / 2 + u]);
+          const u64 p = pk(ex2_approx(a.x), ex2_approx(a.y));
+          l[i / 2 + u] = add2(l[i / 2 + u], p);
+          const float2 w = up(mul2(p, vs2));
           // cut off, not rounded: what a part leaves is exact; mid is stored negated
-          hi[u] = bf16x2_top(up(w));
-          const float2 r = bf16x2_sub(hi[u], up(w));
+          hi[u] = bf16x2_top(w);
+          const float2 r = bf16x2_sub(hi[u], w);
           mid[u] = bf16x2_top(r);
           lo[u] = bf16x2_top(bf16x2_sub(mid[u], r));
         }
@@ -707,6 +724,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           float* dst = dst0 + (c0 + lane) * kPartStride;
           dst[0] = -nm[c0 + lane];
           dst[1] = sum;
+          dst[2] = static_cast<float>(E);
         }
         pos.next_head(d);
       }

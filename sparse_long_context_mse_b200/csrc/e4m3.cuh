@@ -6,11 +6,6 @@
 
 namespace losa {
 
-// Scales below this are taken as this: the smallest one the library writes,
-// and the smallest one whose reciprocal times a row's sum of weights (at most
-// 2^27 keys) stays finite in fp32.
-constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
-
 // Two fp32 values -> two e4m3 codes (round to nearest even; beyond 448 and
 // infinities -> 448; NaN -> NaN), `lo` in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

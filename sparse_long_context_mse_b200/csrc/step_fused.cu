@@ -1937,10 +1937,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (Q8) {
 #pragma unroll 1
-    for (int i = tid; i < nlp; i += kThreads) {
-      const float2 sc = i == tid ? my_scales : page_scales(i);
-      psc[i] = make_float2(sc.x, fmaxf(sc.y, kMinScale));
-    }
+    for (int i = tid; i < nlp; i += kThreads) psc[i] = i == tid ? my_scales : page_scales(i);
   }
   __syncthreads();
 

@@ -10,7 +10,7 @@ import torch
 from losa_testutil import DEV
 from quant_testutil import dense_reference, gpu_dense_quant
 from sparse_long_context_mse_b200 import api
-from test_gpu_quant_attention import inputs
+from test_gpu_quant_attention import gpu_step_quant, inputs, state_of
 
 pytestmark = pytest.mark.gpu
 
@@ -35,7 +35,7 @@ SHAPES = [("bf16", [700], 2, 4, 16), ("bf16", [20000], 8, 4, 1), ("bf16", [9000,
           ("bf16", [1000], 1, 8, 4), ("f32", [3000], 2, 4, 4), ("f32", [700, 90], 1, 8, 16)]
 
 
-@pytest.mark.parametrize("amp", [1e-2, 1e-4, 1e-9])
+@pytest.mark.parametrize("amp", [1e-2, 1e-4, 1e-9, 1e-20])
 @pytest.mark.parametrize("dtype,lens,Hkv,G,B", SHAPES)
 def test_small_values_beside_pages_of_zeros(dtype, lens, Hkv, G, B, amp):
     """A page of zeros has scale 1, whatever its neighbours have, and a share of the weight.
@@ -101,3 +101,66 @@ def test_scales_and_scores_against_each_other(dtype):
         got, ref = run(sh, cache, q[0], kb, torch.zeros_like(vb))
         t = 0.7 * up + 3  # (as above)
         assert errors(got, ref)[0] <= 2.0 ** -20 + t * 20 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype,n,Hkv,G,B", [("bf16", 140000, 1, 1, 1), ("f32", 131072, 1, 1, 1),
+                                             ("bf16", 20000, 148, 1, 16)])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -120, 2.0 ** -100, 2.0 ** 119])
+def test_the_smallest_and_largest_v_scales(dtype, n, Hkv, G, B, scale):
+    """All V scales of a head the same, many keys of one score: the normaliser is their number
+    and the output their mean, at any scale.  148 heads: one CTA has all keys of a head."""
+    sh, cache, _, q, kb, vb = inputs(dtype, [64], Hkv, G, B, seed=3)
+    sh = api.make_shape(1, Hkv * G, Hkv, 128, n, 16, B, 0, 0, dtype, scale=128 ** -0.5)
+    cache = api.alloc_quant_prefix(sh, DEV)
+    cache[1].view(torch.uint8).fill_(0x7E)  # 448
+    cache[2].zero_()
+    cache[3].fill_(scale)
+    got = gpu_dense_quant(sh, torch.zeros_like(q[0]), cache, kb, torch.zeros_like(vb))
+    # equal weights: sums of equal numbers, rounded a few times in fp32 (and truncated 24 times
+    # a tile): 2^-18 in all
+    assert (got["l_p"].double() - math.log(n)).abs().max().item() <= 2.0 ** -20 * math.log(n)
+    assert (got["lse"].double() - math.log(n + B)).abs().max().item() <= 2.0 ** -20 * math.log(n)
+    o = got["o_p"].double()
+    assert torch.isfinite(got["out"]).all()
+    if scale == 0.0:
+        assert (o == 0).all()
+    else:
+        assert (o / (448 * scale) - 1).abs().max().item() <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("per_tile", [6, -6])
+@pytest.mark.parametrize("dtype,B", [("bf16", 16), ("bf16", 1), ("f32", 4)])
+def test_values_that_grow_or_shrink_along_the_prefix(dtype, B, per_tile):
+    """Values 2^6 larger (smaller) from one 128 keys to the next, over 2^66 in all, with scores
+    that make up for it and with flat ones: six tiles for each CTA."""
+    sh, cache, _, q, kb, vb = inputs(dtype, [1500], 74, 1, B, seed=81)
+    for flat in (False, True):
+        g = torch.Generator().manual_seed(9)
+        K, V = (torch.randn(1, 74, 1500, 128, generator=g) for _ in range(2))
+        step = per_tile * (torch.arange(1500) // 128 - 5.5)
+        V *= torch.exp2(step)[:, None]
+        K[..., 0] = 0.0 if flat else -step * math.log(2) / (8 * 128 ** -0.5)
+        api.quantize_prefix(sh, K.to(sh.torch_dtype).to(DEV), V.to(sh.torch_dtype).to(DEV), *cache)
+        q[0][..., 0] = 8.0
+        got, ref = run(sh, cache, q[0], kb, torch.zeros_like(vb))
+        t = 3 if flat else 0.7 * 33 + 3  # (as above)
+        assert errors(got, ref)[0] <= 2.0 ** -20 + t * 20 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -100, 2.0 ** -60, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_step_v_scales(dtype, scale):
+    """The step takes the V scales as they are: every token active on all pages is the dense
+    pass, within 2^-20 of the results' norm (test_step_error_against_64_bits)."""
+    sh, cache, meta, q, kb, vb = inputs(dtype, [60], 2, 4, 8, seed=85, A=8, budget=64)
+    cache[3].fill_(scale)
+    o, l = state_of(sh, 4)
+    r = gpu_step_quant(sh, q[1], q[0], cache, meta, kb, vb, o, l)
+    assert api.read_device_status(r["ws"]) == api.LOSA_OK
+    ref = dense_reference(sh, q[1], *cache, kb, vb)[0]
+    got = r["o_p"].cpu().double()
+    if scale == 0.0:
+        assert (got == 0).all()
+    else:
+        assert ((got - ref["o_p"]).norm() / ref["o_p"].norm()).item() <= 2.0 ** -20
+    assert (r["l_p"].cpu().double() - ref["l_p"]).abs().max().item() <= 2.0 ** -19
