@@ -185,38 +185,46 @@ __global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH
     // a batch raises the maximum
     const float* p0 = part + (first * rows + r) * kPartStride;
     const size_t pstride = static_cast<size_t>(rows) * kPartStride;
-    float M = -INFINITY, lsum = 0.f, E = -126.f;
+    float M = -INFINITY, lsum = 0.f;
+    int E = -126;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int s0 = 0; s0 < nparts; s0 += BATCH) {
-      float mc[BATCH], lc[BATCH], ec[BATCH];
+      float mc[BATCH], lc[BATCH];
       float4 ac[BATCH];
+      // (PAIR: lane i has the maximum, normaliser and E of the batch's partial i, and
+      // works out its weight)
+      const bool has = lane < BATCH && s0 + lane < nparts;
+      float4 hd = make_float4(-INFINITY, 0.f, __int_as_float(-126), 0.f);
+      if (PAIR && has) hd = __ldcg(reinterpret_cast<const float4*>(p0 + (s0 + lane) * pstride));
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
         mc[i] = -INFINITY;
         if (s0 + i < nparts) {
           const float* src = p0 + (s0 + i) * pstride;
-          if (PAIR) {
-            const float4 hd = __ldcg(reinterpret_cast<const float4*>(src));
-            mc[i] = hd.x;
-            lc[i] = hd.y;
-            ec[i] = hd.z;
-          } else {
+          if (!PAIR) {
             mc[i] = __ldcg(src);
             lc[i] = __ldcg(src + 1);
           }
           ac[i] = __ldcg(reinterpret_cast<const float4*>(src + 4) + lane);
         }
       }
-      float Mh = M, Eh = E;
+      float Mh = M, ra, mine = 0.f;
+      if (PAIR) {
+        Mh = fmaxf(M, redux_max(hd.x));
+        const int ec = __float_as_int(hd.z);
+        const int Eh = max(E, __reduce_max_sync(0xffffffffu, ec));
+        const float w = has ? exp2f(hd.x - Mh) : 0.f, rs = exp2f(M - Mh);
+        mine = w * exp2_int(max(ec - Eh, -126));
+        lsum = lsum * rs + warp_sum(w * hd.y);
+        ra = rs * exp2_int(max(E - Eh, -126));
+        E = Eh;
+      } else {
 #pragma unroll
-      for (int i = 0; i < BATCH; ++i) {
-        Mh = fmaxf(Mh, mc[i]);
-        if (PAIR && s0 + i < nparts) Eh = fmaxf(Eh, ec[i]);
+        for (int i = 0; i < BATCH; ++i) Mh = fmaxf(Mh, mc[i]);
+        ra = exp2f(M - Mh);  // 0 while nothing is accumulated
+        lsum *= ra;
       }
-      const float rs = exp2f(M - Mh);  // 0 while nothing is accumulated
-      const float ra = PAIR ? rs * exp2f(E - Eh) : rs;
-      lsum *= rs;
       acc.x *= ra;
       acc.y *= ra;
       acc.z *= ra;
@@ -224,23 +232,21 @@ __global__ void __launch_bounds__(kFinishWarps * (PAIR ? 64 : 32), PAIR && BATCH
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
         if (s0 + i < nparts) {
-          const float w = exp2f(mc[i] - Mh);
-          const float wa = PAIR ? w * exp2f(ec[i] - Eh) : w;
-          lsum += w * lc[i];
-          acc.x += wa * ac[i].x;
-          acc.y += wa * ac[i].y;
-          acc.z += wa * ac[i].z;
-          acc.w += wa * ac[i].w;
+          const float w = PAIR ? __shfl_sync(0xffffffffu, mine, i) : exp2f(mc[i] - Mh);
+          if (!PAIR) lsum += w * lc[i];
+          acc.x += w * ac[i].x;
+          acc.y += w * ac[i].y;
+          acc.z += w * ac[i].z;
+          acc.w += w * ac[i].w;
         }
       }
       M = Mh;
-      E = Eh;
     }
     const float inv = 1.f / lsum;
     float4 op = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     float Lp = (M + __log2f(lsum)) * kLn2;
     if (PAIR) {
-      const float unit = exp2_int(static_cast<int>(E));
+      const float unit = exp2_int(E);
       op = make_float4(op.x * unit, op.y * unit, op.z * unit, op.w * unit);
       // (an 8-bit pass's reference may lie below the row's maximum: the whole numbers of
       // the two logarithms are added first)

@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
           float* dst = dst0 + (c0 + lane) * kPartStride;
           dst[0] = -nm[c0 + lane];
           dst[1] = sum;
-          dst[2] = static_cast<float>(E);
+          dst[2] = __int_as_float(E);
         }
         pos.next_head(d);
       }
