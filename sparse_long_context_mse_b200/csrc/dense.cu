@@ -9,8 +9,7 @@
 // the dense suffix over the block's own keys and writes cache and output.
 // bf16 runs on the 5th-generation tensor cores (tcgen05, TMEM), fp32 on
 // CUDA cores.
-#include <mutex>
-
+#include "device_once.h"
 #include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
@@ -755,18 +754,17 @@ extern "C" int losa_dense_prefix(const losa_shape* shape, const void* q, const v
   int* status = reinterpret_cast<int*>(static_cast<char*>(workspace) + d.off_status);
   if (d.dtype == LOSA_BF16) {
     if (d.G * d.B > 128) return LOSA_ERR_UNSUPPORTED;
-    static bool attr_done[kMaxDevices] = {};
+    static DeviceOnce<kMaxDevices> attrs;
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 0 && dev < kMaxDevices && !attr_done[dev]) {
-      cudaError_t e0 = cudaFuncSetAttribute(
+    const cudaError_t e0 = attrs.run(dev, [] {
+      const cudaError_t e64 = cudaFuncSetAttribute(
           dense_umma_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, UPlan<64>::smem);
-      if (e0 == cudaSuccess)
-        e0 = cudaFuncSetAttribute(dense_umma_kernel<128>,
+      if (e64 != cudaSuccess) return e64;
+      return cudaFuncSetAttribute(dense_umma_kernel<128>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize, UPlan<128>::smem);
-      if (e0 != cudaSuccess) return record_cuda_error(e0);
-      attr_done[dev] = true;
-    }
+    });
+    if (e0 != cudaSuccess) return record_cuda_error(e0);
     const bool m64 = d.G * d.B <= 64;
     CUtensorMap qmap, kmap, vmap;
     if (make_tmap(&qmap, q, rows, m64 ? 64 : 128) != LOSA_OK ||

@@ -60,6 +60,7 @@
 // range), floor 85 us: 267 us, the same softmax.  In loops of more than a few
 // milliseconds the 64-row passes draw the card's 1000 W and the clock falls from
 // 1.92 to 1.65 GHz: 48 and 316 us.
+#include "device_once.h"
 #include "e4m3.cuh"
 #include "losa_common.cuh"
 #include "ptx.cuh"
@@ -743,14 +744,13 @@ int launch_partials(const Dims& d, const void* q, const void* k8, const void* v8
                     cudaStream_t st) {
   using C = QPlan<NR, NQ>;
   auto* fn = dense_quant_kernel<NR, NQ>;
-  static bool attr_done[kMaxDevices] = {};
+  static DeviceOnce<kMaxDevices> attrs;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= kMaxDevices || !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
-    if (e != cudaSuccess) return record_cuda_error(e);
-    if (dev >= 0 && dev < kMaxDevices) attr_done[dev] = true;
-  }
+  const cudaError_t e = attrs.run(dev, [&] {
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  });
+  if (e != cudaSuccess) return record_cuda_error(e);
   CUtensorMap kmap, vmap;
   const unsigned long long nrows = static_cast<unsigned long long>(d.S) * d.Hkv * d.Lc;
   if (make_byte_tmap(&kmap, k8, nrows, kLineKeys) != LOSA_OK ||
