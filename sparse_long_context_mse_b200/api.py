@@ -15,6 +15,8 @@ from typing import Optional
 
 import torch
 
+from .build import binding_name
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblosa.so")
 
@@ -377,9 +379,9 @@ def _native():
     """The native checks (raises if they were not built)."""
     global _binding
     if _binding is None:
-        path = os.path.join(_PKG, "_binding.so")
+        path = os.path.join(_PKG, binding_name())
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
+            raise RuntimeError(f"{path} is missing: build it (for this torch and Python) with "
                                "`python -m sparse_long_context_mse_b200.build`")
         spec = importlib.util.spec_from_file_location("_binding", path)
         m = importlib.util.module_from_spec(spec)

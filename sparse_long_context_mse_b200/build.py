@@ -1,5 +1,6 @@
 """Build step of the CUDA library: ``csrc/*.cu`` -> ``liblosa.so`` (in-tree), and
-of the binding's native argument checks: ``csrc/torch_binding.cpp`` -> ``_binding.so``.
+of the binding's native argument checks: ``csrc/torch_binding.cpp`` ->
+``_binding.<torch and Python it is built for>.so``.
 
 nvcc cross-compiles for sm_100a; no GPU is needed to build.
 ``python -m sparse_long_context_mse_b200.build`` rebuilds when a source or
@@ -13,13 +14,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblosa.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 OBJDIR = os.path.join(ROOT, "_build")
 
@@ -51,25 +52,34 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_name():
+    """File name of the native argument checks for this Python and torch: they are
+    compiled against torch's C++ classes, so another version's are another file."""
+    import torch
+    return "_binding.torch-%s.cxx11abi-%d%s" % (
+        torch.__version__.replace("+", "-"), torch._C._GLIBCXX_USE_CXX11_ABI,
+        sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def _binding_deps():
     return [BINDING_SRC, os.path.join(INCLUDE, "losa.h"), os.path.abspath(__file__)]
 
 
 def _binding_stale() -> bool:
-    return not os.path.exists(BINDING) or any(
-        os.path.getmtime(p) > os.path.getmtime(BINDING) for p in _binding_deps())
+    path = os.path.join(PKG, binding_name())
+    return not os.path.exists(path) or any(
+        os.path.getmtime(p) > os.path.getmtime(path) for p in _binding_deps())
 
 
-def build_binding(force: bool = False) -> str:
+def build_binding(force: bool = False):
     """The native argument checks, against the installed torch's headers."""
+    path = os.path.join(PKG, binding_name())
     if not force and not _binding_stale():
-        return BINDING
-    import sysconfig
-
+        return path
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    tmp = BINDING + ".tmp.%d" % os.getpid()
+    tmp = path + ".tmp.%d" % os.getpid()
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-isystem", inc, "-isystem", cuda,
            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, BINDING_SRC, "-o", tmp,
@@ -78,8 +88,8 @@ def build_binding(force: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{res.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 TRACE_LIB = os.path.join(PKG, "liblosa_trace.so")
