@@ -2,7 +2,8 @@
 of the binding's native argument checks: ``csrc/torch_binding.cpp`` ->
 ``_binding.<torch and Python it is built for>.so``.
 
-nvcc cross-compiles for sm_100a; no GPU is needed to build.
+nvcc cross-compiles for sm_100a; no GPU is needed to build.  The library needs no
+torch; without one the native argument checks are left out.
 ``python -m sparse_long_context_mse_b200.build`` rebuilds when a source or
 header is newer than the library.
 """
@@ -54,8 +55,12 @@ def up_to_date() -> bool:
 
 def binding_name():
     """File name of the native argument checks for this Python and torch: they are
-    compiled against torch's C++ classes, so another version's are another file."""
-    import torch
+    compiled against torch's C++ classes, so another version's are another file.
+    None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     return "_binding.torch-%s.cxx11abi-%d%s" % (
         torch.__version__.replace("+", "-"), torch._C._GLIBCXX_USE_CXX11_ABI,
         sysconfig.get_config_var("EXT_SUFFIX"))
@@ -66,14 +71,22 @@ def _binding_deps():
 
 
 def _binding_stale() -> bool:
-    path = os.path.join(PKG, binding_name())
+    name = binding_name()
+    if name is None:
+        return False
+    path = os.path.join(PKG, name)
     return not os.path.exists(path) or any(
         os.path.getmtime(p) > os.path.getmtime(path) for p in _binding_deps())
 
 
 def build_binding(force: bool = False):
-    """The native argument checks, against the installed torch's headers."""
-    path = os.path.join(PKG, binding_name())
+    """The native argument checks, against the installed torch's headers: their path,
+    or None without torch."""
+    name = binding_name()
+    if name is None:
+        sys.stderr.write("no torch: the native argument checks are not built\n")
+        return None
+    path = os.path.join(PKG, name)
     if not force and not _binding_stale():
         return path
     import torch
@@ -100,9 +113,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
     """The library; with ``trace`` a separate copy, ``liblosa_trace.so``,
     whose step kernel records per-phase timestamps (``phase_trace.py``)."""
     lib = TRACE_LIB if trace else LIB
-    build_binding(force)
     if not force and os.path.exists(lib) and all(
             os.path.getmtime(p) <= os.path.getmtime(lib) for p in _deps()):
+        build_binding(force)
         return lib
     objdir = os.path.join(OBJDIR, "trace") if trace else OBJDIR
     os.makedirs(objdir, exist_ok=True)
@@ -126,6 +139,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False,
     tmp = lib + ".tmp.%d" % os.getpid()
     subprocess.check_call([cc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, lib)
+    build_binding(force)
     return lib
 
 
