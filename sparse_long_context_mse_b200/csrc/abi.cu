@@ -15,10 +15,6 @@ namespace losa {
 namespace {
 thread_local std::string g_last_error;
 
-// The workspace is sized for the B200's SM count so that sizes do not depend
-// on which device happens to be current (and can be queried without one).
-constexpr int kSizingSms = 148;
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 

@@ -714,14 +714,19 @@ int launch_dense_finish(const Dims& d, const void* q, const void* k_blk, const v
     return launch_behind(fn, grid, 32 * warps, smem, st, q, k_blk, v_blk, part, o_p, l_p, out, out_lse, d);
   };
   if (!d.line_ctas) return launch(dense_finish_kernel<false, 18>, kFinishWarps);
-  // 8-bit prefix.  A KV head has about line_ctas / (S Hkv) partials per row: where
-  // they are many (few heads, so few CTAs here) one round of 18 loads per row ends
-  // first, else three small CTAs per SM.  A pass with single warps, with rounds of
-  // 18 and with rounds of 6: 8 KV heads, 64 rows, 64K prefix (19 partials) 43.1, 41.5
-  // and 43.2 us; 8K 16.8, 15.3 and 16.0; 8 x 32K, 128 rows (2 or 3) 289, 291 and 268;
-  // one token for 8 ragged sequences (3 or 4) 50.7, 54.5 and 50.3.
-  return d.line_ctas > 8 * d.S * d.Hkv ? launch(dense_finish_kernel<true, 18>, 2 * kFinishWarps)
-                                       : launch(dense_finish_kernel<true, 6>, 2 * kFinishWarps);
+  // 8-bit prefix.  A row has about line_ctas / (S Hkv) partials.  Rounds of 18 loads (one
+  // CTA per SM) end first while the partials are more than one round of 6 and all CTAs
+  // run at once; else rounds of 6, three CTAs per SM.  us a pass with rounds of 18 and of
+  // 6, 4 query heads per KV head: one sequence, B = 16: 1 KV head, 16K (128 partials) 22.5
+  // and 30.3; 4, 64K (37) 31.5 and 34.5; 8, 64K (18) 44.5 and 46.6; B = 1: 13.1 and 14.9
+  // at 4 heads of 16K.  Ragged (16384, 9000, 3), 8 heads (6 or 7, 8 of the longest): B = 1
+  // (96 CTAs) 30.1 and 31.6, B = 16 (384) 65.9 and 60.7.  4 x 16K, 4 heads (9): B = 1 (64)
+  // 19.2 and 19.8, B = 16 (256) 31.4 and 29.5.  4 x 4K, 8 heads (4): B = 1 (128) 13.4 and
+  // 12.9.  fp32 alike.
+  const bool wide = d.line_ctas > 6 * d.S * d.Hkv &&
+                    static_cast<long long>(grid.x) * grid.y <= kSizingSms;
+  return wide ? launch(dense_finish_kernel<true, 18>, 2 * kFinishWarps)
+              : launch(dense_finish_kernel<true, 6>, 2 * kFinishWarps);
 }
 }  // namespace losa
 

@@ -21,6 +21,9 @@ constexpr int kMaxRowsPerGroup = 128;  // G*B (and hence G*A) per KV head
 constexpr int kMaxK = 64;       // pages per active row unless every page is taken
 constexpr int kPartStride = kD + 4;    // floats per split-softmax partial: m, l, pad, pad, acc[d]
 constexpr int kMaxDevices = 64;
+// The B200's SM count: sizes and launch shapes do not depend on which device happens
+// to be current (and sizes can be queried without one).
+constexpr int kSizingSms = 148;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

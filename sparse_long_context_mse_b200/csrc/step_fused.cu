@@ -2448,7 +2448,11 @@ int launch_fused_step(const Dims& d, const void* q_cur, const void* q_prev, cons
   // 8 stages, 32 us), so clusters of 4 or 2 CTAs, of which two or four times as
   // many run at once, can be faster.  Measured with clusters of 8, 4 and 2 (8 KV
   // heads): 4 sequences of 16K 86, 37, 56 us; 8 of 16K 145, 74, 58; 3 of 64K 73,
-  // 57, 137; 8 of 2K 40 each (their plan has few CTAs anyhow).
+  // 57, 137; 8 of 2K 40 each (their plan has few CTAs anyhow).  fp32 steps take longer
+  // and compare the same way (4 x 16K 205, 125, 223; 8 x 16K 336, 244, 225; 4 x 48K 342,
+  // 219, 418): over both types, 1, 2, 4 and 8 query heads per KV head, 2, 4 and 8 KV heads,
+  // 3 to 32 sequences of 1K to 48K the choice was the fastest of the three, or within the
+  // clock's 2 us of it, in all 52 shapes tried.
   bool planned = false;
   if (d.quant && room.c8 > 0 && NG > room.c8) {
     int best = 0;
