@@ -147,9 +147,9 @@ int make_dims(const losa_shape* sh, int which, Dims* d) {
     // time (its pipeline drains, the next queries are staged).  Sequences of one
     // length can be cut at KV heads, with a whole number of CTAs for each: better
     // while the longest range grows by less than that.  Measured, even ranges and
-    // cut ones: 8 KV heads, 64 rows: 64K prefix 45.7 and 43.1 us, 8K 19.0 and 16.7;
-    // 8 sequences of 32K, 128 rows, where the cut makes a range 34 tiles longer:
-    // 285 and 318 us, not cut.
+    // cut ones: 8 KV heads, 64 rows: 64K prefix 50.4 and 47.8 us, 8K 19.4 and 15.7;
+    // fp32 59.2 and 55.5; 4 rows 32.1 and 30.7; 8 sequences of 32K, 128 rows, where the
+    // cut makes a range 34 tiles longer: 299 and 325 us, not cut.
     const long long per = d->line_ctas / static_cast<long long>(SG);
     if (!d->lens && per > 0) {
       const long long nt = tiles / static_cast<long long>(SG);

@@ -32,17 +32,18 @@
 //   a row's weight need not be what its output is made of (a page or a token of
 //   zeros, values far smaller than another page's), so a weight keeps its own
 //   relative accuracy, however far it lies below the reference.  (Two fp16 parts
-//   are cheaper -- 64 rows, 64K prefix 49.2 us in place of 53.3 -- and have 22 bits,
-//   but only of weights within 2^-13 of the largest; below 2^-36 they are zero.)  V8 has to be bf16 too.  Four warps transpose V codes out of
-//   shared memory (ldmatrix, bytes), widen them (exact) and store them as the A
-//   operand in TMEM, which costs 1/8 of the shared-memory traffic of a 16-bit tile
-//   there; W goes through shared memory as the MN-major B.
+//   are cheaper -- 64 rows, 64K prefix 43 us in place of 47 -- and have 22 bits, but
+//   only of weights within 2^-13 of the largest; below 2^-36 they are zero.)  V8 has
+//   to be bf16 too.  Four warps transpose V codes out of shared memory (ldmatrix,
+//   bytes), widen them (exact) and store them as the A operand in TMEM, which costs
+//   1/8 of the shared-memory traffic of a 16-bit tile there; W goes through shared
+//   memory as the MN-major B.
 // * A softmax thread owns one key (TMEM lane) and 8 or 16 of the query columns:
 //   the page scales are constants of the thread, l is a sum in registers across tiles
 //   (joined over the lanes at the end), and no tile needs a maximum over the
-//   lanes: the reference moves only when some w would pass 2^15, which one
+//   lanes: the reference moves only when some p would pass 2^4, which one
 //   barrier with a vote finds out.
-// * The tensor core's accumulator truncates (up to 2^-24 of it on each of the 16
+// * The tensor core's accumulator truncates (up to 2^-24 of it on each of the 24
 //   steps of a tile, all in one direction: 1.4e-5 after 800 of them, measured),
 //   so O stays in it for one tile only and is summed in registers.
 // * All SMs get the same number of tiles, whatever the lengths and the number of
@@ -50,16 +51,15 @@
 //
 // Measured, calls back to back (with the finish kernel; the floor at the copy
 // bandwidth of 6.45 TB/s): 8 KV heads, 64K prefix, 134 MB, floor 21 us: 16 rows
-// per KV head 31.7 us, 32 rows 33.0, 64 rows 42.0.  Up to 32 rows it is bound by
-// the loads (what is left of it with the softmax taken out takes 28 us: 23 for
-// the bytes, and a prologue and an end that no tile overlaps).  With 64 rows a
-// tile's 2000 cycles go to the softmax warps: 8192 weights, each scaled, voted
-// on, raised to a power of two and split in two fp16 numbers, some 5200 warp
-// instructions at 0.65 a cycle and scheduler, with no pipe above 40 % busy and
-// the tensor core at 33 %.  Eight sequences of 32K and 128 rows (two CTAs each
-// range), floor 85 us: 267 us, the same softmax.  In loops of more than a few
-// milliseconds the 64-row passes draw the card's 1000 W and the clock falls from
-// 1.92 to 1.65 GHz: 48 and 316 us.
+// per KV head 31.1 us, 32 rows 35.4, 64 rows 47.0; fp32 38.2, 41.1, 54.4.  With 16
+// rows it is bound by the loads (what is left of it with the softmax taken out takes
+// 28 us: 23 for the bytes, and a prologue and an end that no tile overlaps).  With 64
+// rows a tile's 2300 cycles go to the softmax warps and to widening V: 8192 weights,
+// each scaled, voted on, raised to a power of two and split in three, and 16384
+// codes, some 6300 warp instructions at 62 % of the issue slots, the tensor core at
+// 40 %.  Eight sequences of 32K and 128 rows (two CTAs each range), floor 85 us: 296
+// us, the same.  In loops of more than a few milliseconds the 64-row passes draw the
+// card's 1000 W and the clock falls from 1.92 to 1.65 GHz: 52 and 346 us.
 #include "device_once.h"
 #include "e4m3.cuh"
 #include "losa_common.cuh"
@@ -114,10 +114,13 @@ template <int NR, int NQ>
 struct QPlan {
   // A tile is a chain of dependent waits and instructions for a softmax warp, and
   // the longer the more columns it has, so the columns are spread over as many
-  // warps as the registers allow: 16 columns per thread at most (64 rows, 64K
-  // prefix: 51 us a pass with four warp groups, 59 with two; one CTA with 128
-  // columns in place of two with 64: 346 us for 8 x 32K, against 293).
-  static constexpr int nwg = NR > 32 ? 4 : 2;            // softmax warp groups
+  // warps as the registers allow: 16 columns per thread at most, 8 with 32 columns
+  // of bf16 queries (64K prefix, 8 KV heads: 35.7 us a pass with four warp groups,
+  // 37.2 with two; fp32, with a second score accumulator to read, 42.9 and 41.8).
+  // Measured while weights had two parts: 64 columns in four warp groups 51 us, in two
+  // 59; one CTA with 128 columns in place of two with 64 346 us for 8 x 32K, against
+  // 293.
+  static constexpr int nwg = NR > 32 || (NR == 32 && NQ == 2) ? 4 : 2;  // softmax warp groups
   static constexpr int soft = nwg * 128;                 // .. threads
   static constexpr int threads = soft + 256;
   // the softmax warps take registers over from the others
@@ -793,8 +796,8 @@ extern "C" int losa_dense_prefix_quant(const losa_shape* shape, const void* q, c
   float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + d.off_part);
   int* status = reinterpret_cast<int*>(static_cast<char*>(workspace) + d.off_status);
   // the fewest columns that hold the rows: what a tile costs beyond its loads
-  // grows with them (8 KV heads, 64K prefix, 16 rows: 31.6 us with 16 columns,
-  // 33.2 with 32, 40.6 with 64; fp32 36.1, 37.1, 46.4)
+  // grows with them (8 KV heads, 64K prefix, 16 rows: 31.2 us with 16 columns,
+  // 35.1 with 32, 45.4 with 64; fp32 38.4, 40.7, 52.1)
   const int r = d.G * d.B;
   auto* launch = d.dtype == LOSA_BF16 ? (r <= 16   ? launch_partials<16, 2>
                                          : r <= 32 ? launch_partials<32, 2>
