@@ -345,6 +345,10 @@ int losa_dequantize_prefix(const losa_shape* shape, const void* k8, const void* 
  * is the attention of one decoded token.  Same arguments and results, with the
  * prefix as codes and scales.
  *
+ * The scores come from 8-bit parts of each query row: with bf16 queries an element
+ * down to 2^-13 of its row's largest is taken exactly and a smaller one to within
+ * 2^-21 of that largest, with fp32 queries every element to within 2^-29 of it.
+ *
  *   workspace  >= losa_workspace_size(shape, LOSA_WS_DENSE_QUANT) bytes,
  *              256-byte aligned; contents on entry are irrelevant.
  */
