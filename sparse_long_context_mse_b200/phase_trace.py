@@ -7,7 +7,9 @@ the step.  Runs a few steps of a synthetic workload through the public API
 with that library and prints, per phase, the minimum / median / maximum
 over the CTAs of the time since the first CTA started (microseconds).
 
-    python -m sparse_long_context_mse_b200.phase_trace [workload ...]
+    python -m sparse_long_context_mse_b200.phase_trace [--quant] [workload ...]
+
+``--quant``: the step over the prefix in 8 bits.
 
 The product library is not touched: this module only imports ``api`` with
 its library path pointed at the tracing build, in its own process.
@@ -59,9 +61,10 @@ def _lib():
     return api, L
 
 
-def trace(name: str, reps: int = 3, n_layers: int = 2):
+def trace(name: str, reps: int = 3, n_layers: int = 2, quant: bool = False):
     """Per-phase (min, median, max) microseconds of ``reps`` steps of the
-    workload ``name`` (the last rep's table is returned, all are printed)."""
+    workload ``name`` (the last rep's table is returned, all are printed);
+    ``quant``: over the prefix in 8 bits."""
     import torch
     from sparse_long_context_mse_b200 import synth
     api, L = _lib()
@@ -84,13 +87,17 @@ def trace(name: str, reps: int = 3, n_layers: int = 2):
         out, lse = torch.empty_like(o_p), torch.empty_like(l_p)
         api.dense_prefix(sh, q[0], pre["k_prefix"], pre["v_prefix"], kv[0][0], kv[0][1], o_p, l_p,
                          out, lse, ws_dense)
-        layers.append((pre, q, kv, meta, o_p, l_p, out, lse))
+        cache = (pre["k_prefix"], pre["v_prefix"])
+        if quant:
+            cache = api.alloc_quant_prefix(sh, dev)
+            api.quantize_prefix(sh, pre["k_prefix"], pre["v_prefix"], *cache, meta)
+        layers.append((cache, q, kv, meta, o_p, l_p, out, lse))
 
     def step(i):
-        pre, q, kv, meta, o_p, l_p, out, lse = layers[i % n_layers]
+        cache, q, kv, meta, o_p, l_p, out, lse = layers[i % n_layers]
         t = 1 + i % (T - 1)
-        api.step(sh, q[t], q[t - 1], pre["k_prefix"], pre["v_prefix"], meta, kv[t][0], kv[t][1],
-                 o_p, l_p, out, lse, ws)
+        (api.step_quant if quant else api.step)(sh, q[t], q[t - 1], *cache, meta, kv[t][0],
+                                                kv[t][1], o_p, l_p, out, lse, ws)
 
     for i in range(6):  # warm-up
         step(i)
@@ -120,5 +127,6 @@ def trace(name: str, reps: int = 3, n_layers: int = 2):
 
 if __name__ == "__main__":
     from sparse_long_context_mse_b200 import synth
-    for n in sys.argv[1:] or [synth.GQA64K]:
-        trace(n)
+    names = [a for a in sys.argv[1:] if a != "--quant"]
+    for n in names or [synth.GQA64K]:
+        trace(n, quant="--quant" in sys.argv[1:])
