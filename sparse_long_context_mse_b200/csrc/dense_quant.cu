@@ -2,14 +2,15 @@
 //
 // The page scales are factors of a key's score and of its value.  In base 2, with
 // x_j = scale * ks(page j) * (q . k8_j) * log2(e), a reference m per row and a power
-// of two 2^E near the largest V scale, the kernel accumulates
+// of two 2^E, 2^40 below the largest V scale, the kernel accumulates
 //
 //   p_j = 2^(x_j - m),   l = sum_j p_j,   W_j = p_j vs(page j) 2^-E,
 //   O = sum_j W_j v8_j,   o = 2^E O / l,
 //
 // E is that of the first tile of a KV head's keys and moves, as a reference does, when
-// a tile's largest scale passes 2^(E + 32): nothing overflows or loses bits while the
-// V scales of a head's keys lie within 2^100 of each other, whatever their size.
+// a tile's largest scale passes 2^(E + 40 + 32): nothing overflows, whatever the size of
+// the V scales, and a key keeps all of its bits while p is a normal number (2^-126) and
+// p vs is not below 2^-140 of the largest V scale.
 //
 // Its floor is HBM: 256 bytes per key and KV head, read once.  The work is laid
 // out so that little on the chip takes longer:
@@ -75,9 +76,11 @@ namespace {
 constexpr int kTileBytes = kLineKeys * kD;  // one K or V tile of codes: 16 KB
 constexpr int kVCols = kLineKeys / 2;       // TMEM columns of a V^T tile (bf16 pairs)
 // A row's reference is its largest score when it is set, and stays until a weight would
-// pass 2^4; E likewise.  So O stays below 2^(4 + 33 + 9) per key.
+// pass 2^4; E likewise.  So a key adds at most 2^(4 + 33 + 40 + 9) to O, and 2^30 keys
+// (more than the card has memory for) stay below 2^116; a weight of 2^-100 still has
+// its third part above bf16's smallest number.
 constexpr float kRefMove = 4.f;
-constexpr int kScaleMove = 32;
+constexpr int kScaleMove = 32, kScaleUp = 40;
 constexpr float kPartScale = 4096.f;        // fp32: parts 4-6 are this much larger
 
 typedef unsigned long long u64;
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(QPlan<NR, NQ>::threads, 1)
         const int nv = min(kLineKeys, pos.L - pos.lt * kLineKeys);
         // (non-negative floats are ordered like their bits)
         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v_, 0.f)));
-        const int e = min(max(static_cast<int>(top >> 23) - 127, -126), 126);
+        const int e = max(static_cast<int>(top >> 23) - 127 - kScaleUp, -126);
         if (it == 0 || pos.lt == 0 || e > E + kScaleMove) E = e;
         pos.next(d);
         const bool last = it + 1 == n || pos.lt == 0;

@@ -164,3 +164,27 @@ def test_step_v_scales(dtype, scale):
     else:
         assert ((got - ref["o_p"]).norm() / ref["o_p"].norm()).item() <= 2.0 ** -20
     assert (r["l_p"].cpu().double() - ref["l_p"]).abs().max().item() <= 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype,lens,Hkv,G,B", [("bf16", [700], 2, 4, 8), ("f32", [300, 90], 1, 8, 4)])
+def test_the_smallest_weights(dtype, lens, Hkv, G, B):
+    """Tokens of zeros hold all but 2^-116 of the weight: the other keys' weights, down to fp32's
+    smallest normal number, keep their bits.  Rows are compared by direction (the factor that
+    a row has in common is the heavy tokens' score, summed to within 2^-13).  An exponent of
+    64 to 128 is rounded by at most half of 2^-17, which is ln 2 * 2^-18 of the weight; the
+    rest is 2^-20 (test_dense_error_against_64_bits)."""
+    sh, cache, _, q, kb, vb = inputs(dtype, lens, Hkv, G, B, seed=sum(lens) + 13)
+    g = torch.Generator().manual_seed(6)
+    K, V = (torch.randn(len(lens), Hkv, sh.capacity, 128, generator=g) for _ in range(2))
+    K *= 0.5  # (scores within 2^+-5 of 2^-116)
+    K[..., 0] = 0.0
+    heavy = torch.arange(5, sh.capacity, 64)
+    K[:, :, heavy, 0] = 116 * math.log(2) / (8 * 128 ** -0.5)
+    V[:, :, heavy] = 0.0
+    api.quantize_prefix(sh, K.to(sh.torch_dtype).to(DEV), V.to(sh.torch_dtype).to(DEV), *cache)
+    q[0][..., 0] = 8.0
+    got, ref = run(sh, cache, q[0], kb, torch.zeros_like(vb))
+    a, b = got["o_p"].cpu().double(), ref["o_p"]
+    assert (b.norm(dim=-1) > 0).all()
+    a, b = a / a.norm(dim=-1, keepdim=True), b / b.norm(dim=-1, keepdim=True)
+    assert (a - b).norm(dim=-1).max().item() <= math.log(2) * 2.0 ** -18 + 2.0 ** -20
