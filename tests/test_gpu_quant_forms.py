@@ -171,3 +171,30 @@ def test_dense_of_one_head_among_many_rows():
         sh, cache, _, q, kb, vb = inputs("bf16", [700], 1, G, B, seed=G)
         got = gpu_dense_quant(sh, q[0], cache, kb, vb)
         check_dense(got, *dense_reference(sh, q[0], *cache, kb, vb), f"{G} {B}")
+
+
+@pytest.mark.parametrize("dtype,L,Hkv", [("bf16", 131072, 8), ("bf16", 131069, 4), ("f32", 65530, 4)])
+def test_long_prefix(dtype, L, Hkv):
+    """The longest prefix that the framework's own workloads have: the step against the one
+    over the read-back prefix (bounds as in test_step_equals_the_step_over_the_read_back_prefix),
+    the dense pass against 64 bits, and a block appended behind it."""
+    B = 16
+    sh, cache, meta, q, kb, vb = inputs(dtype, [L], Hkv, 4, B, L + 20, 17, A=4, budget=128)
+    got = gpu_dense_quant(sh, q[0], cache, kb, vb)
+    check_dense(got, *dense_reference(sh, q[0], *cache, kb, vb))
+    K, V = (torch.zeros(1, Hkv, sh.capacity, 128, dtype=sh.torch_dtype, device=DEV) for _ in range(2))
+    for _ in range(2):
+        api.dequantize_prefix(sh, *cache, K, V)
+        o, l = state_of(sh, 3)
+        a = gpu_step_quant(sh, q[1], q[0], cache, meta, kb, vb, o.clone(), l.clone())
+        b = gpu_step(sh, q[1], q[0], K, V, meta, kb, vb, o.clone(), l.clone())
+        assert api.read_device_status(a["ws"]) == api.LOSA_OK
+        for key in KEYS:
+            if dtype == "bf16" and key in ("o_p", "out"):
+                vmax = max(V.abs().max().item(), vb.abs().max().item(), o.abs().max().item())
+                assert (a[key] - b[key]).abs().max().item() <= 2.0 ** -14 * vmax, key
+            else:
+                assert torch.equal(a[key], b[key]), key
+        if sh.prefix_len == L:
+            api.append_block_quant(sh, kb, vb, *cache, meta)
+            sh.prefix_len += B
