@@ -292,10 +292,11 @@ int losa_step_ref(const losa_shape* shape, const void* q_cur, void* q_ref,
  * The calls that read a cache take any finite scales, also ones written by
  * another program, of which the V scales are >= 0 (zeros among them).  The
  * attention calls are accurate for V scales of 2^-100 and more, the dense pass
- * while those of a KV head lie within 2^100 of each other.  There a key whose
- * weight is below 2^-126 of its row's largest counts as none, as the smallest
- * numbers of fp32 do.  Scales and codes of pages and tokens past a sequence's
- * length are never used, whatever they hold, and never written.
+ * while those of a KV head lie within 2^100 of each other.  A key counts as none
+ * where fp32 ends: in the dense pass where its weight is below 2^-126 of its
+ * row's largest, in the step where that ratio times its V scale is (and there
+ * it has fewer bits from 2^-110 on).  Scales and codes of pages and tokens past
+ * a sequence's length are never used, whatever they hold, and never written.
  * Scale arrays need the alignment of a float only (a layer's slice of a larger
  * array), the other buffers 16 bytes as everywhere. */
 
